@@ -69,7 +69,10 @@ enum nvq_dtype { NVQ_F32 = 0, NVQ_BF16 = 1 };
 /* device status bits (nvq_device_status) */
 enum {
   NVQ_STATUS_NONFINITE = 1u << 0, /* a quantized input held Inf or NaN */
-  NVQ_STATUS_BAD_EXPERT = 1u << 1 /* a top-k expert id was outside [0, E) */
+  NVQ_STATUS_BAD_EXPERT = 1u << 1, /* a top-k expert id was outside [0, E) */
+  NVQ_STATUS_BAD_SLOT = 1u << 2,   /* a cache slot was past the last page */
+  NVQ_STATUS_BAD_SEQUENCE = 1u << 3 /* a page id, length or row range of a sequence does not
+                                       fit the cache, the block table or the query rows */
 };
 
 const char* nvq_status_string(int status);
@@ -409,6 +412,161 @@ typedef struct nvq_qat_gemm_args {
 
 size_t qat_gemm_workspace_bytes(int64_t rows, int64_t E);
 int qat_fakequant_gemm_w4a16(const nvq_qat_gemm_args* args, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rotary positions of projected heads (the step before the FP4 KV cache of
+ * the rollout, TRACE "Résultats"; the gradient is the trainer's side of it).
+ *
+ * Token t, head h, pair j of rot_dim / 2, angle a = positions[t] * inv_freq[j]:
+ *   y_u = m (x_u cos a - x_w sin a),  y_w = m (x_u sin a + x_w cos a)
+ * with (u, w) = (j, j + rot_dim / 2) for NVQ_ROPE_HALF and (2j, 2j + 1) for
+ * NVQ_ROPE_INTERLEAVED; elements at or past rot_dim are copied.  inverse != 0
+ * turns by -a with the same m: the gradient of the forward call.
+ *
+ * x, y      [T, H, D] of dtype NVQ_F32 or NVQ_BF16, unit element stride; token
+ *           t, head h of x starts at element t * x_ld_t + h * x_ld_h (0 means
+ *           dense: H * D and D), of y likewise.  y == x with equal strides
+ *           works in place (then elements past rot_dim are not touched); any
+ *           other overlap is not supported.  No alignment beyond the element's
+ *           is required; 16-byte aligned rows with rot_dim % 16 == 0 (bf16) or
+ *           % 8 (fp32), D a multiple of 8 (bf16) or 4, take the vector path.
+ * positions [T] int32, any value.  inv_freq [rot_dim / 2] fp64, radians per
+ *           position.  Angles are reduced in fp64 (their error stays below
+ *           2^-20 radians at every int32 position), sine, cosine and the
+ *           products are fp32, rounded once to dtype.
+ * 2 <= rot_dim <= D <= 4096, rot_dim even, H <= 65535, T < 2^24; the
+ * rows of y do not overlap.
+ * Asynchronous on stream; errors (NVQ_EINVAL, NVQ_ESHAPE, NVQ_EALIGN) launch
+ * nothing; T == 0 or H == 0 does nothing. */
+enum { NVQ_ROPE_HALF = 0, NVQ_ROPE_INTERLEAVED = 1 };
+int nvq_rope(const void* x, int dtype, int64_t T, int64_t H, int64_t D, int64_t x_ld_t,
+             int64_t x_ld_h, const int32_t* positions, const double* inv_freq, int64_t rot_dim,
+             int layout, float magnitude, int inverse, void* y, int64_t y_ld_t, int64_t y_ld_h,
+             void* stream);
+
+/* Frequencies of the rotation, written to HOST memory: inv_freq [rot_dim / 2]
+ * fp64 with f_j = base^(-2j / rot_dim), stretched for long contexts by kind:
+ *   NVQ_ROPE_PLAIN   f_j
+ *   NVQ_ROPE_LINEAR  f_j / factor (positions divided by factor)
+ *   NVQ_ROPE_BASE    f_j of the base base * factor^(rot_dim / (rot_dim - 2)),
+ *                    which leaves the fastest pair and divides the slowest by
+ *                    factor (rot_dim > 2)
+ *   NVQ_ROPE_RAMP    r f_j + (1 - r) f_j / factor, r = clamp((n_j - slow) /
+ *                    (fast - slow), 0, 1) with n_j = orig_len f_j / (2 pi) the
+ *                    pair's turns over the original context (0 < slow < fast);
+ *                    *magnitude = 0.1 ln(factor) + 1.
+ * *magnitude (nullable) is 1 for the other kinds.  factor >= 1, base > 0 (> 1
+ * for NVQ_ROPE_BASE).  No HIP call.  NVQ_EINVAL / NVQ_ESHAPE. */
+enum { NVQ_ROPE_PLAIN = 0, NVQ_ROPE_LINEAR = 1, NVQ_ROPE_BASE = 2, NVQ_ROPE_RAMP = 3 };
+int nvq_rope_frequencies(int kind, int64_t rot_dim, double base, double factor, double orig_len,
+                         double slow, double fast, double* inv_freq, float* magnitude);
+
+/* ------------------------------------------------------------------------ */
+/* Paged NVFP4 KV cache (TRACE "Résultats": FP4 weights, activations and KV
+ * cache in the rollout).
+ *
+ * One layer's K and V as two NVFP4 records with 16-element blocks along the
+ * head dimension and one static tensor scale each, in num_pages pages of
+ * page_size slots.  Slot s is offset s % page_size of page s / page_size; the
+ * slots of one (page, head) are contiguous.  V keeps its block scales with
+ * the slots innermost, because attention contracts over the slots there: the
+ * scales of one block of consecutive keys come with one load.
+ * All buffers are device memory of the caller; codes and k_scales, v_scales
+ * 16-byte aligned.  page_size is a power of two, 16 <= page_size <= 65536;
+ * head_dim % 16 == 0, 16 <= head_dim <= 512; 1 <= heads <= 65535;
+ * num_pages >= 1.  Contents never written may hold any bytes. */
+typedef struct nvq_kv_cache {
+  size_t struct_size;          /* sizeof(nvq_kv_cache) */
+  uint8_t* k_codes;            /* [num_pages, heads, page_size, head_dim / 2] */
+  uint8_t* k_scales;           /* [num_pages, heads, page_size, head_dim / 16] */
+  uint8_t* v_codes;            /* [num_pages, heads, page_size, head_dim / 2] */
+  uint8_t* v_scales;           /* [num_pages, heads, head_dim / 16, page_size] */
+  const float* k_tensor_scale; /* [1] s_t of K (amax / 2688) */
+  const float* v_tensor_scale; /* [1] s_t of V */
+  int64_t num_pages;
+  int32_t page_size, heads, head_dim;
+} nvq_kv_cache;
+
+/* Quantizes T new tokens as it writes them: k and v [T, heads, head_dim] of
+ * dtype NVQ_F32 or NVQ_BF16 (token t, head h at element t * ld_t + h * ld_h, 0
+ * meaning dense; rows 16-byte aligned) go to slots[t].  The bytes are those of
+ * nvfp4_quantize with the cache's tensor scales (exact decisions; values past
+ * 2688 s_t saturate).  A negative slot skips the token; a slot past the last
+ * page skips it and sets NVQ_STATUS_BAD_SLOT; a non-finite value sets
+ * NVQ_STATUS_NONFINITE (its block is unspecified).  Slots that no token names
+ * keep their bytes.  The slots of one call should differ: where two tokens
+ * name one slot, each of its bytes is one of theirs.
+ * ws nullable (else 256-byte aligned, >= 256 bytes): receives the status word.
+ * T < 2^24; num_pages * page_size <= INT32_MAX.  Asynchronous on stream;
+ * errors (NVQ_EINVAL, NVQ_ESHAPE, NVQ_EALIGN, NVQ_EWORKSPACE) launch nothing. */
+int nvq_kv_append(const nvq_kv_cache* cache, const void* k, const void* v, int dtype, int64_t T,
+                  int64_t k_ld_t, int64_t k_ld_h, int64_t v_ld_t, int64_t v_ld_h,
+                  const int32_t* slots, void* ws, size_t ws_bytes, void* stream);
+
+/* Reads T slots back: k_out and v_out [T, heads, head_dim] dense, of dtype
+ * out_dtype, receive sign * fl32(fl32(G s_b) s_t) (rounded to nearest-even for
+ * NVQ_BF16), as nvfp4_dequantize gives it.  Either output may be NULL; they
+ * are 16-byte aligned.  A negative slot gives zeros; a slot past the last
+ * page gives zeros and sets NVQ_STATUS_BAD_SLOT.  A slot may be read any
+ * number of times.  ws and limits as for nvq_kv_append. */
+int nvq_kv_gather(const nvq_kv_cache* cache, const int32_t* slots, int64_t T, void* k_out,
+                  void* v_out, int out_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of a chunk of new tokens over the paged cache, for single decoded
+ * tokens, drafted tokens and prompt chunks alike.
+ *
+ * Sequence b owns the query rows cu_q[b] .. cu_q[b + 1] - 1 and the keys 0 ..
+ * kv_len[b] - 1; key j lies in slot j % page_size of page block_table[b,
+ * j / page_size].  Row i of its n is at position p = kv_len[b] - n + i (the
+ * new tokens are the last ones, already appended).  Query head h reads
+ * key/value head h / (q_heads / heads).  With K^, V^ the dequantized record:
+ *   out[row, h] = sum_j w_j V^[j],  w = softmax_j(softmax_scale q . K^[j])
+ * over the visible keys: j <= p if causal (every key of the sequence if not),
+ * and j > p - window if window > 0 (causal only).  A row without visible keys
+ * gives zeros and lse = -inf.  lse [total_q, q_heads] (nullable) receives the
+ * natural logarithm of the sum of exponentials.
+ * q is bf16; q . K^ is summed in fp32 from exact products (q is held in fp16
+ * under a power of two per row), the softmax is fp32, its weights are rounded
+ * to fp16 for the product with V^ (2^-11 relative), out is rounded to bf16.
+ *
+ * Rows that no sequence owns (before cu_q[0], from cu_q[B] on) are not
+ * written.  A page id outside [0, num_pages), keys past the block table's
+ * width, kv_len < 0, a decreasing or too large cu_q, or more than max_q rows
+ * in a sequence set NVQ_STATUS_BAD_SEQUENCE in the workspace's status word:
+ * such keys are left out, a negative length counts as 0, ranges are cut to
+ * [0, total_q] and rows past the max_q-th are not written.  No call reads or
+ * writes outside its buffers for any content of the index arrays.  Sequences
+ * may share pages.  Calls on one stream may share a workspace. */
+typedef struct nvq_paged_attention_args {
+  size_t struct_size;          /* sizeof(nvq_paged_attention_args) */
+  int64_t total_q, B;          /* query rows; sequences */
+  int64_t max_q;               /* no sequence has more new tokens; 0: total_q */
+  int32_t q_heads;             /* a multiple of cache->heads */
+  int32_t causal;              /* 0 or 1 */
+  int64_t window;              /* 0: none */
+  float softmax_scale;
+  const uint16_t* q;           /* [total_q, q_heads, head_dim] bf16, 16-byte aligned rows */
+  int64_t q_ld_t, q_ld_h;      /* strides in elements; 0: dense */
+  const int32_t* cu_q;         /* [B + 1] */
+  const int32_t* kv_len;       /* [B] */
+  const int32_t* block_table;  /* [B, table_width], row stride table_ld (0: table_width) */
+  int64_t table_width, table_ld;
+  uint16_t* out;               /* [total_q, q_heads, head_dim] bf16, 16-byte aligned rows */
+  int64_t out_ld_t, out_ld_h;
+  float* lse;                  /* [total_q, q_heads] fp32 or NULL */
+  void* ws;                    /* 256-byte aligned */
+  size_t ws_bytes;
+} nvq_paged_attention_args;
+
+/* Workspace of a call with these arguments (only the sizes are read: total_q,
+ * B, max_q, q_heads, table_width and the cache's heads, head_dim, page_size). */
+size_t nvq_paged_attention_workspace_bytes(const nvq_kv_cache* cache,
+                                           const nvq_paged_attention_args* args);
+/* Limits: total_q < 2^24, q_heads <= 32768, B <= 65535, table_width * page_size <= INT32_MAX.
+ * Errors: NVQ_EINVAL, NVQ_ESHAPE, NVQ_EALIGN, NVQ_EWORKSPACE; nothing is
+ * launched then. */
+int nvq_paged_attention(const nvq_kv_cache* cache, const nvq_paged_attention_args* args,
+                        void* stream);
 
 #ifdef __cplusplus
 }

@@ -24,6 +24,7 @@ EXTRA = {
     "quantize.hip": ["-ffp-contract=off"],
     "moe.hip": ["-ffp-contract=off"],
     "guided.hip": ["-ffp-contract=off"],
+    "kvcache.hip": ["-ffp-contract=off"],
 }
 
 COMMON = [

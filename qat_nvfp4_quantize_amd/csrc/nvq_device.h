@@ -19,6 +19,11 @@ __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f) {
   return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
 
+// The same for any value: a NaN stays one.
+__device__ __forceinline__ uint32_t f32_to_bf16_any(float f) {
+  return f == f ? f32_to_bf16_rne(f) : 0x7FC0u;
+}
+
 // ------------------------------------------------------- wave reductions --
 // Max over the 64 lanes of a wave with DPP row operations and four
 // readlanes; every lane receives the result.  No LDS traffic.

@@ -33,6 +33,10 @@ struct WsCarve {
 inline int hip_status(hipError_t e) { return e == hipSuccess ? NVQ_OK : NVQ_EHIP; }
 inline int last_launch() { return hip_status(hipGetLastError()); }
 
+// Tokens of one call of the rotary and cache entry points: their grids stay
+// below 2^32 threads in x for every size up to it.
+constexpr int64_t kMaxTokens = (1 << 24) - 1;
+
 // Number of compute units of the current device (cached per process).
 int device_cu_count();
 

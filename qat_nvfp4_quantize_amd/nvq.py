@@ -20,7 +20,10 @@ NVQ_EPI_NONE, NVQ_EPI_SWIGLU = 0, 1
 NVQ_GEMM_AUTO, NVQ_GEMM_DEQ16, NVQ_GEMM_FP8_BLOCK, NVQ_GEMM_DEQ16_WIDE = 0, 1, 2, 3
 NVQ_QAT_FWD, NVQ_QAT_DGRAD, NVQ_QAT_WGRAD = 0, 1, 2
 NVQ_STATUS_NONFINITE, NVQ_STATUS_BAD_EXPERT = 1, 2
+NVQ_STATUS_BAD_SLOT, NVQ_STATUS_BAD_SEQUENCE = 4, 8
 NVQ_GUIDE_MANTISSA, NVQ_GUIDE_DIRECTION = 0, 1
+NVQ_ROPE_HALF, NVQ_ROPE_INTERLEAVED = 0, 1
+NVQ_ROPE_PLAIN, NVQ_ROPE_LINEAR, NVQ_ROPE_BASE, NVQ_ROPE_RAMP = 0, 1, 2, 3
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -59,6 +62,24 @@ class QatGemmArgs(ctypes.Structure):
     ]
 
 
+class KvCacheArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", _SZ), ("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P),
+        ("k_tensor_scale", _P), ("v_tensor_scale", _P), ("num_pages", _I64), ("page_size", _I32),
+        ("heads", _I32), ("head_dim", _I32),
+    ]
+
+
+class PagedAttentionArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", _SZ), ("total_q", _I64), ("B", _I64), ("max_q", _I64), ("q_heads", _I32),
+        ("causal", _I32), ("window", _I64), ("softmax_scale", ctypes.c_float), ("q", _P),
+        ("q_ld_t", _I64), ("q_ld_h", _I64), ("cu_q", _P), ("kv_len", _P), ("block_table", _P),
+        ("table_width", _I64), ("table_ld", _I64), ("out", _P), ("out_ld_t", _I64),
+        ("out_ld_h", _I64), ("lse", _P), ("ws", _P), ("ws_bytes", _SZ),
+    ]
+
+
 # (name, restype, argtypes)
 _SIGS = [
     ("nvq_status_string", ctypes.c_char_p, [ctypes.c_int]),
@@ -89,6 +110,19 @@ _SIGS = [
     ("moe_grouped_gemm_w4a4_comp", ctypes.c_int, [ctypes.POINTER(MoeGemmArgs), _P]),
     ("qat_gemm_workspace_bytes", _SZ, [_I64, _I64]),
     ("qat_fakequant_gemm_w4a16", ctypes.c_int, [ctypes.POINTER(QatGemmArgs), _P]),
+    ("nvq_rope", ctypes.c_int,
+     [_P, ctypes.c_int, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, ctypes.c_int, ctypes.c_float,
+      ctypes.c_int, _P, _I64, _I64, _P]),
+    ("nvq_rope_frequencies", ctypes.c_int,
+     [ctypes.c_int, _I64] + [ctypes.c_double] * 5 + [_P, ctypes.POINTER(ctypes.c_float)]),
+    ("nvq_kv_append", ctypes.c_int,
+     [ctypes.POINTER(KvCacheArgs), _P, _P, ctypes.c_int, _I64, _I64, _I64, _I64, _I64, _P, _P, _SZ, _P]),
+    ("nvq_kv_gather", ctypes.c_int,
+     [ctypes.POINTER(KvCacheArgs), _P, _I64, _P, _P, ctypes.c_int, _P, _SZ, _P]),
+    ("nvq_paged_attention_workspace_bytes", _SZ,
+     [ctypes.POINTER(KvCacheArgs), ctypes.POINTER(PagedAttentionArgs)]),
+    ("nvq_paged_attention", ctypes.c_int,
+     [ctypes.POINTER(KvCacheArgs), ctypes.POINTER(PagedAttentionArgs), _P]),
 ]
 
 EXPORTED = [s[0] for s in _SIGS]
@@ -487,3 +521,220 @@ def qat_fakequant_gemm_w4a16(mode, w_codes, w_scales, w_tensor_scale, expert_off
     if mode == NVQ_QAT_WGRAD:
         return dw
     return ob, of
+
+
+# ------------------------------------------ rotary positions, paged KV cache --
+def _same_device(dev, **tensors):
+    """Every given tensor lies on the GPU `dev`."""
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be a GPU tensor on {dev}, got {t.device}")
+
+
+def _typed(t, name, dtype, *shape):
+    """A contiguous tensor of this dtype and (where given) shape."""
+    if t.dtype != dtype or not t.is_contiguous() or (shape and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be contiguous {dtype}" + (f" {list(shape)}" if shape else "")
+                         + f", got {t.dtype} {list(t.shape)}")
+    return t
+
+
+def _heads(t, name, dtypes):
+    """(T, H, D, ld_t, ld_h) of [T, H, D] projected heads with unit element
+    stride, tokens and heads strided freely (a slice of a fused projection)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != 3 or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be [T, H, D] of {dtypes}, got {t.dtype} {list(t.shape)}")
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (T > 1 and st <= 0) or (H > 1 and sh <= 0):
+        raise ValueError(f"{name} must have unit element stride and no broadcast axis, got "
+                         f"strides {t.stride()}")
+    # the stride of an axis of one is free: 0 stands for the dense one
+    return T, H, D, (st if T > 1 else 0), (sh if H > 1 else 0)
+
+
+class _Device:
+    """Makes `dev` the current device for a call, and gives its current stream."""
+
+    def __init__(self, dev):
+        self.dev = dev
+        self.guard = None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.dev.index:
+            self.guard = torch.cuda.device(self.dev)
+            self.guard.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream(self.dev).cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+_HEAD_TYPES = (torch.bfloat16, torch.float32)
+
+
+def nvq_rope_frequencies(rot_dim, base=10000.0, kind=NVQ_ROPE_PLAIN, factor=1.0, orig_len=0.0,
+                         slow=1.0, fast=32.0):
+    """(inv_freq fp64 [rot_dim / 2] on the CPU, magnitude): the rotation's
+    radians a position, stretched for long contexts by kind."""
+    f = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.float64)
+    m = ctypes.c_float(1.0)
+    _check("nvq_rope_frequencies", load().nvq_rope_frequencies(
+        kind, rot_dim, base, factor, orig_len, slow, fast, f.data_ptr() or None, ctypes.byref(m)))
+    return f, m.value
+
+
+def nvq_rope(x, positions, inv_freq, interleaved=False, magnitude=1.0, inverse=False, out=None):
+    """x [T, H, D] (bf16/fp32, tokens and heads may be strided) with the first
+    2 * len(inv_freq) elements of each head turned by positions [T] int32 times
+    inv_freq (fp64, on the GPU); inverse turns back (the gradient).  out: a
+    tensor like x to write, x itself for in place."""
+    T, H, D, ld_t, ld_h = _heads(x, "x", _HEAD_TYPES)
+    if out is None:
+        out = torch.empty(T, H, D, dtype=x.dtype, device=x.device)
+        old_t = old_h = 0
+    else:
+        if out.shape != x.shape or out.dtype != x.dtype:
+            raise ValueError("out must have the shape and dtype of x")
+        _, _, _, old_t, old_h = _heads(out, "out", _HEAD_TYPES)
+    _typed(positions, "positions", torch.int32, T)
+    _typed(inv_freq, "inv_freq", torch.float64)
+    _same_device(x.device, positions=positions, inv_freq=inv_freq, out=out)
+    with _Device(x.device) as stream:
+        _check("nvq_rope", load().nvq_rope(
+            x.data_ptr(), _dtype_code(x), T, H, D, ld_t, ld_h, positions.data_ptr(),
+            inv_freq.data_ptr(), 2 * inv_freq.numel(), int(bool(interleaved)), magnitude,
+            int(bool(inverse)), out.data_ptr(), old_t, old_h, stream))
+    return out
+
+
+class KvCache:
+    """The paged NVFP4 cache of one layer over the caller's buffers: k_codes,
+    v_codes u8 [pages, heads, page_size, D/2], k_scales u8 [pages, heads,
+    page_size, D/16], v_scales u8 [pages, heads, D/16, page_size], and the
+    tensor scales k_scale, v_scale fp32 [1]."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, k_scale, v_scale):
+        if not k_codes.is_cuda or k_codes.dim() != 4:
+            raise ValueError("k_codes must be a GPU tensor [pages, heads, page_size, D/2]")
+        P, H, S, half = k_codes.shape
+        D = 2 * half
+        _typed(k_codes, "k_codes", torch.uint8)
+        _typed(v_codes, "v_codes", torch.uint8, P, H, S, half)
+        _typed(k_scales, "k_scales", torch.uint8, P, H, S, D // 16)
+        _typed(v_scales, "v_scales", torch.uint8, P, H, D // 16, S)
+        _typed(k_scale, "k_scale", torch.float32, 1)
+        _typed(v_scale, "v_scale", torch.float32, 1)
+        self.device = k_codes.device
+        _same_device(self.device, k_scales=k_scales, v_codes=v_codes, v_scales=v_scales,
+                     k_scale=k_scale, v_scale=v_scale)
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.num_pages, self.heads, self.page_size, self.head_dim = P, H, S, D
+        self.args = KvCacheArgs(ctypes.sizeof(KvCacheArgs), k_codes.data_ptr(), k_scales.data_ptr(),
+                                v_codes.data_ptr(), v_scales.data_ptr(), k_scale.data_ptr(),
+                                v_scale.data_ptr(), P, S, H, D)
+
+    @classmethod
+    def empty(cls, num_pages, heads, page_size, head_dim, k_amax, v_amax, device="cuda"):
+        """A cache of uninitialised pages whose tensor scales are calibrated to
+        the given amax values (s_t = amax / 2688)."""
+        def u8(*shape):
+            return torch.empty(num_pages, heads, *shape, dtype=torch.uint8, device=device)
+
+        # the fp32 quotient of nvfp4_quantize: rounded once from fp64
+        st = (torch.tensor([k_amax, v_amax], dtype=torch.float32).double() / 2688.0).float().to(device)
+        return cls(u8(page_size, head_dim // 2), u8(page_size, head_dim // 16),
+                   u8(page_size, head_dim // 2), u8(head_dim // 16, page_size), st[0:1].clone(),
+                   st[1:2].clone())
+
+
+def nvq_kv_append(cache, k, v, slots, ws=None):
+    """Quantizes the new tokens k, v [T, heads, D] (bf16/fp32, tokens and heads
+    may be strided) into the cache's slots [T] int32 (page * page_size + offset,
+    negative: skipped).  ws (optional, >= 256 bytes) receives the status word."""
+    T, H, D, k_t, k_h = _heads(k, "k", _HEAD_TYPES)
+    Tv, Hv, Dv, v_t, v_h = _heads(v, "v", _HEAD_TYPES)
+    if (T, H, D) != (Tv, Hv, Dv) or k.dtype != v.dtype or (H, D) != (cache.heads, cache.head_dim):
+        raise ValueError(f"k and v must be [T, {cache.heads}, {cache.head_dim}] of one dtype, got "
+                         f"{k.dtype} {list(k.shape)} and {v.dtype} {list(v.shape)}")
+    _typed(slots, "slots", torch.int32, T)
+    _same_device(cache.device, k=k, v=v, slots=slots, ws=ws)
+    with _Device(cache.device) as stream:
+        _check("nvq_kv_append", load().nvq_kv_append(
+            ctypes.byref(cache.args), k.data_ptr(), v.data_ptr(), _dtype_code(k), T, k_t, k_h, v_t, v_h,
+            slots.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(), stream))
+
+
+def nvq_kv_gather(cache, slots, out_dtype=torch.bfloat16, out=None, ws=None):
+    """(k, v) [T, heads, D] read back from the cache's slots [T] int32 (a
+    negative slot: zeros).  ws (optional) receives the status word."""
+    T = slots.numel()
+    _typed(slots, "slots", torch.int32, T)
+    shape = (T, cache.heads, cache.head_dim)
+    if out is None:
+        if out_dtype not in _HEAD_TYPES:
+            raise ValueError(f"unsupported dtype {out_dtype}")
+        k = torch.empty(shape, dtype=out_dtype, device=cache.device)
+        v = torch.empty(shape, dtype=out_dtype, device=cache.device)
+    else:
+        k, v = out
+        _typed(k, "k", k.dtype, *shape)
+        _typed(v, "v", k.dtype, *shape)
+    _same_device(cache.device, slots=slots, k=k, v=v, ws=ws)
+    with _Device(cache.device) as stream:
+        _check("nvq_kv_gather", load().nvq_kv_gather(
+            ctypes.byref(cache.args), slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), _dtype_code(k),
+            _ptr(ws), 0 if ws is None else ws.numel(), stream))
+    return k, v
+
+
+def nvq_paged_attention(q, cache, cu_q, kv_len, block_table, max_q=None, scale=None, causal=True,
+                        window=0, lse=None, out=None, ws=None):
+    """Attention of the new tokens q [total_q, q_heads, D] (bf16, tokens and
+    heads may be strided) over the cache: sequence b owns rows cu_q[b] ..
+    cu_q[b + 1] - 1 and keys 0 .. kv_len[b] - 1, in the pages block_table[b].
+    cu_q [B + 1], kv_len [B], block_table [B, width] int32 (rows may be
+    strided).  max_q: no sequence has more new tokens (default: all of them).
+    scale defaults to D^-1/2.  lse: optional fp32 [total_q, q_heads] to receive
+    the log-sum-exp.  Returns out, bf16 like q."""
+    T, Hq, D, ld_t, ld_h = _heads(q, "q", (torch.bfloat16,))
+    if D != cache.head_dim:
+        raise ValueError(f"q must have the cache's head_dim {cache.head_dim}, got {D}")
+    B = kv_len.numel()
+    _typed(cu_q, "cu_q", torch.int32, B + 1)
+    _typed(kv_len, "kv_len", torch.int32, B)
+    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype != torch.int32 or (
+            block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table must be int32 [{B}, width] with unit column stride")
+    width = block_table.shape[1]
+    table_ld = block_table.stride(0) if B > 1 else width
+    if B > 1 and table_ld < width:
+        raise ValueError("block_table rows must not overlap")
+    if out is None:
+        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
+        o_t = o_h = 0
+    else:
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+        _, _, _, o_t, o_h = _heads(out, "out", (torch.bfloat16,))
+    if lse is not None:
+        _typed(lse, "lse", torch.float32, T, Hq)
+    _same_device(cache.device, q=q, cu_q=cu_q, kv_len=kv_len, block_table=block_table, out=out, lse=lse,
+                 ws=ws)
+    a = PagedAttentionArgs(
+        ctypes.sizeof(PagedAttentionArgs), T, B, 0 if max_q is None else max_q, Hq, int(bool(causal)),
+        window, D ** -0.5 if scale is None else scale, q.data_ptr(), ld_t, ld_h, cu_q.data_ptr(),
+        kv_len.data_ptr(), block_table.data_ptr(), width, table_ld, out.data_ptr(), o_t, o_h,
+        None if lse is None else lse.data_ptr(), None, 0)
+    L = load()
+    with _Device(cache.device) as stream:
+        if ws is None:
+            ws = workspace(L.nvq_paged_attention_workspace_bytes(ctypes.byref(cache.args), ctypes.byref(a)),
+                           cache.device)
+        a.ws, a.ws_bytes = ws.data_ptr(), ws.numel()
+        _check("nvq_paged_attention", L.nvq_paged_attention(ctypes.byref(cache.args), ctypes.byref(a), stream))
+    return out
