@@ -13,6 +13,7 @@
 #include <cmath>
 
 #include "nvq.h"
+#include "nvq_attn.h"
 #include "nvq_device.h"
 #include "nvq_internal.h"
 #include "nvq_kv.h"
@@ -20,73 +21,6 @@
 
 namespace nvq {
 namespace {
-
-struct AttnParams {
-  KvPages c;
-  const uint16_t* q;
-  uint16_t* out;
-  float* lse;
-  const int32_t *cu_q, *kv_len, *table;
-  int64_t q_ld_t, q_ld_h, out_ld_t, out_ld_h, table_ld;
-  int64_t window;    // 0: none
-  int64_t num_keys;  // keys a row of the block table covers
-  int total_q, B, max_q, Hq, g;
-  int causal;
-  float scale_log2;  // softmax_scale * log2(e)
-  uint32_t* status;
-};
-
-constexpr float kLn2 = 0.69314718055994530942f;
-
-// Rows and keys of sequence b, cut to what the call's buffers hold.
-struct Seq {
-  int row0, n;   // query rows
-  int64_t len;   // keys
-  int64_t pos0;  // position of the first row: the rows are the last positions
-};
-__device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
-  Seq s;
-  s.row0 = min(max(p.cu_q[b], 0), p.total_q);
-  const int n = max(min(p.cu_q[b + 1], p.total_q) - s.row0, 0);
-  s.n = min(n, p.max_q);
-  s.len = max(p.kv_len[b], 0);
-  s.pos0 = s.len - n;
-  return s;
-}
-
-// Visible keys [lo, hi) of the query at position pos.
-__device__ __forceinline__ void visible(const AttnParams& p, const Seq& s, int64_t pos, int64_t& lo, int64_t& hi) {
-  hi = min(p.causal ? pos + 1 : s.len, min(s.len, p.num_keys));
-  lo = p.window > 0 ? max<int64_t>(pos - p.window + 1, 0) : 0;
-}
-
-// One workgroup looks over the index arrays and writes the status word:
-// lengths and row ranges of every sequence, and the page id of every page
-// that some query row of it can see.  It runs beside the others, which only
-// stay inside the buffers, so no atomic and no clearing is needed.
-__device__ __forceinline__ void check_batch(const AttnParams& p, uint32_t* s_flag) {
-  if (threadIdx.x == 0) *s_flag = 0u;
-  __syncthreads();
-  bool bad = false;
-  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-    const int64_t r0 = p.cu_q[b], r1 = p.cu_q[b + 1], len = p.kv_len[b];
-    bad |= r0 < 0 || r1 < r0 || r1 > p.total_q || r1 - r0 > p.max_q || len < 0 || (r1 > r0 && len > p.num_keys);
-  }
-  for (int b = 0; b < p.B; ++b) {
-    const Seq s = load_seq(p, b);
-    if (s.n == 0) continue;
-    int64_t lo, hi, x;
-    visible(p, s, s.pos0, lo, x);
-    visible(p, s, s.len - 1, x, hi);
-    for (int64_t i = (lo >> p.c.log_ps) + threadIdx.x; (i << p.c.log_ps) < hi; i += blockDim.x) {
-      const int32_t id = p.table[b * p.table_ld + i];
-      bad |= id < 0 || id >= p.c.num_pages;
-    }
-  }
-  if (bad) atomicOr(s_flag, (uint32_t)NVQ_STATUS_BAD_SEQUENCE);
-  __syncthreads();
-  if (threadIdx.x == 0) *p.status = *s_flag;
-}
 
 // ----------------------------------------------------------- any head size --
 // One workgroup per query row and head, its four waves taking 64 keys each in
@@ -216,12 +150,21 @@ int attn_sizes(const nvq_kv_cache* cache, const nvq_paged_attention_args* a, Att
   if (cache->heads < 1 || ps < 16 || ps > 65536 || a->q_heads < 1 || a->q_heads > 32768 ||
       a->q_heads % cache->heads)
     return NVQ_ESHAPE;
-  if (a->table_width > INT32_MAX / ps) return NVQ_ESHAPE;
+  if (a->table_width > INT32_MAX / ps || a->B * cache->heads > (1 << 22)) return NVQ_ESHAPE;
   p.total_q = (int)a->total_q, p.B = (int)a->B;
   p.max_q = (int)(a->max_q == 0 ? a->total_q : std::min(a->max_q, a->total_q));
   p.Hq = a->q_heads, p.g = a->q_heads / cache->heads;
   p.num_keys = a->table_width * ps;
+  p.c.H = cache->heads, p.c.D = cache->head_dim;
   return NVQ_OK;
+}
+
+// Lays the workspace out; returns its bytes.
+size_t attn_plan(const AttnParams& p, void* ws, RowsPlan& rows) {
+  WsCarve c(ws);
+  rows.max_rows = 0;
+  if (const int tiles = attn_rows_tiles(p.c.D, (int64_t)p.max_q * p.g)) attn_rows_plan(p, tiles, c, rows);
+  return c.off;
 }
 
 }  // namespace
@@ -233,7 +176,8 @@ extern "C" size_t nvq_paged_attention_workspace_bytes(const nvq_kv_cache* cache,
                                                       const nvq_paged_attention_args* args) {
   AttnParams p{};
   if (attn_sizes(cache, args, p)) return kAlign;
-  return kAlign;
+  RowsPlan rows;
+  return attn_plan(p, nullptr, rows);
 }
 
 extern "C" int nvq_paged_attention(const nvq_kv_cache* cache, const nvq_paged_attention_args* args, void* stream) {
@@ -262,7 +206,8 @@ extern "C" int nvq_paged_attention(const nvq_kv_cache* cache, const nvq_paged_at
     return NVQ_EALIGN;
   if (!a.ws) return NVQ_EINVAL;
   if (!aligned256(a.ws)) return NVQ_EALIGN;
-  if (a.ws_bytes < nvq_paged_attention_workspace_bytes(cache, args)) return NVQ_EWORKSPACE;
+  RowsPlan rows;
+  if (a.ws_bytes < attn_plan(p, a.ws, rows)) return NVQ_EWORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   p.status = static_cast<uint32_t*>(a.ws);
   if (p.total_q == 0 || p.B == 0) return clear_status(p.status, s);
@@ -271,6 +216,7 @@ extern "C" int nvq_paged_attention(const nvq_kv_cache* cache, const nvq_paged_at
   p.cu_q = a.cu_q, p.kv_len = a.kv_len, p.table = a.block_table;
   p.window = a.window, p.causal = a.causal;
   p.scale_log2 = a.softmax_scale * 1.44269504088896340736f;
+  if (rows.max_rows) return attn_rows_launch(p, rows.max_rows / 16, rows, s);
   hipLaunchKernelGGL(k_attn_any, dim3((unsigned)p.total_q, (unsigned)p.Hq + 1), dim3(256), 0, s, p);
   return last_launch();
 }

@@ -1,0 +1,544 @@
+// Attention over the paged NVFP4 cache for sequences of few query rows per
+// key/value head (single tokens, drafts): HBM-bound, the cache's 0.5625 bytes
+// a value are read once and little is done with each.
+//
+// A wave takes 32 keys at a time straight from memory into MFMA operands: no
+// LDS on the way.  Both products run transposed, S^T = K Q^T and O^T = V^T P^T
+// (16x16x32 fp16), so that a lane always holds one query (column) and several
+// keys or elements (rows):
+//  * K: lane (key n, group q) loads the codes of D / 4 consecutive elements,
+//    q D/4 .., of its key; MFMA step w takes its w-th eight.  Any order of
+//    the contraction works because Q is held in the same one.
+//  * S^T leaves lane (query n, q) the keys 16 t + 4 q + v: softmax needs no
+//    lane exchange, and its weights are already the B operand of O^T with the
+//    contraction order (t, v) per lane.
+//  * V: lane (n, q) loads, for those 8 keys, the codes of elements n D/16 ..
+//    n D/16 + D/16 - 1; tile u of O^T takes the u-th of them, so a byte
+//    permute pairs the keys of an element and one packed multiply applies two
+//    block scales (one dword holds the scales of four consecutive slots).
+// The reference of the running softmax is only moved when a score exceeds it
+// by 15 (in powers of two): weights stay within fp16, and a step without a
+// move rescales nothing.
+//
+// Work is split over the keys: the pieces of all sequences are sized from the
+// lengths on the device (every wave computes the same plan from cu_q and
+// kv_len), a workgroup per piece and key/value head, its four waves taking
+// 32 keys of each 128 in turn; pieces of a split sequence are joined by a
+// second kernel.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "nvq.h"
+#include "nvq_attn.h"
+#include "nvq_dequant.h"
+#include "nvq_device.h"
+#include "nvq_internal.h"
+
+namespace nvq {
+namespace {
+
+typedef float floatx4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kUnit = 128;      // keys of a workgroup step: 4 waves x 32
+constexpr float kRefRoom = 15;  // a score may exceed the reference by this (2^15 < fp16's largest)
+constexpr float kRefStart = 9;  // and the reference is set this much below the largest score seen
+
+// Keys [lo, hi) that some row of sequence s sees, in 32-key steps from `base`.
+struct Range {
+  int64_t base, hi;
+  int units;
+};
+__device__ __forceinline__ Range key_range(const AttnParams& p, const Seq& s) {
+  Range r;
+  int64_t lo, x;
+  visible(p, s, s.pos0, lo, x);
+  visible(p, s, s.pos0 + s.n - 1, x, r.hi);
+  r.base = lo & ~(int64_t)31;
+  r.units = r.hi > r.base ? (int)((r.hi - r.base + kUnit - 1) / kUnit) : 1;
+  return r;
+}
+
+__device__ __forceinline__ int64_t wave_sum_i64(int64_t v) {
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) v += __shfl_xor(v, x, 64);
+  return v;
+}
+
+struct Piece {
+  int b, index, count, units;
+};
+
+// Piece `item` of the plan (the same for every key/value head); false past
+// the last one.  All lanes return the same values.
+__device__ __forceinline__ bool find_piece(const AttnParams& p, const RowsPlan& plan, int item, Piece& out) {
+  const int lane = threadIdx.x & 63;
+  auto units_of = [&](int b) -> int {
+    if (b >= p.B) return 0;
+    const Seq s = load_seq(p, b);
+    return (s.n == 0 || s.n * p.g > plan.max_rows) ? 0 : key_range(p, s).units;
+  };
+  const int first = units_of(lane);
+  int64_t total = first;
+  for (int b0 = 64; b0 < p.B; b0 += 64) total += units_of(b0 + lane);
+  total = wave_sum_i64(total);
+  const int64_t per = max<int64_t>((total * p.c.H + plan.target - 1) / plan.target, plan.min_units);
+  int before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 64) {
+    const int units = b0 == 0 ? first : units_of(b0 + lane);
+    const int n = (int)((units + per - 1) / per);
+    int incl = n;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) {
+      const int up = __shfl_up(incl, x, 64);
+      if (lane >= x) incl += up;
+    }
+    const uint64_t past = __ballot(before + incl > item);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      out.b = b0 + l;
+      out.count = __builtin_amdgcn_readlane(n, l);
+      out.index = item - (before + __builtin_amdgcn_readlane(incl, l) - out.count);
+      out.units = __builtin_amdgcn_readlane(units, l);
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return false;
+}
+
+// Codes and scales of one wave step (32 keys) in registers.
+template <int D>
+struct StepRegs {
+  static constexpr int kKW = D / 32;                  // dwords of K codes of a lane and half
+  static constexpr int kVW = D / 128 > 1 ? D / 128 : 1;  // dwords of V codes of a lane and key
+  uint32_t k[2][kKW], ks[2], v[8][kVW], vs[2];
+};
+
+template <int D>
+__device__ __forceinline__ void load_step(const AttnParams& p, StepRegs<D>& r, const int (&id)[2], int kvh, int off0,
+                                          int lane) {
+  const int n = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int64_t tile = ((int64_t)max(id[t], 0) * p.c.H + kvh) << p.c.log_ps;  // a masked page reads page 0
+    const int off = (off0 + 16 * t) & (p.c.ps - 1);
+    const uint8_t* kc = p.c.k_codes + (tile + off) * (D / 2) + n * (D / 2) + q * (D / 8);
+    if constexpr (D == 64) {
+      const uint2 w = *reinterpret_cast<const uint2*>(kc);
+      r.k[t][0] = w.x, r.k[t][1] = w.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 128; ++i) {
+        const uint4 w = reinterpret_cast<const uint4*>(kc)[i];
+        r.k[t][4 * i] = w.x, r.k[t][4 * i + 1] = w.y, r.k[t][4 * i + 2] = w.z, r.k[t][4 * i + 3] = w.w;
+      }
+    }
+    const uint8_t* ks = p.c.k_scales + (tile + off) * (D / 16) + n * (D / 16) + q * (D / 64);
+    if constexpr (D == 64)
+      r.ks[t] = *ks;
+    else if constexpr (D == 128)
+      r.ks[t] = *reinterpret_cast<const uint16_t*>(ks);
+    else
+      r.ks[t] = *reinterpret_cast<const uint32_t*>(ks);
+    const uint8_t* vc = p.c.v_codes + (tile + off + 4 * q) * (D / 2) + n * (D / 32);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* at = vc + i * (D / 2);
+      uint32_t(&w)[StepRegs<D>::kVW] = r.v[4 * t + i];
+      if constexpr (D == 64) {
+        w[0] = *reinterpret_cast<const uint16_t*>(at);
+      } else if constexpr (D == 128) {
+        w[0] = *reinterpret_cast<const uint32_t*>(at);
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(at);
+        w[0] = x.x, w[1] = x.y;
+      }
+    }
+    r.vs[t] = *reinterpret_cast<const uint32_t*>(p.c.v_scales + tile * (D / 16) + ((int64_t)(n * D / 256) << p.c.log_ps) +
+                                                 off + 4 * q);
+  }
+}
+
+template <int kSel>
+__device__ __forceinline__ uint32_t fp4_pair_f16(uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, kSel));
+}
+
+// Two elements (byte kSel of each key's codes) of 8 keys -> the A operands of
+// two tiles: element e of keys 0..7 times the keys' block scales.
+template <int kSel>
+__device__ __forceinline__ void v_operands(const uint32_t (&w)[8], const half2_t (&sc)[4], half8_t& lo, half8_t& hi) {
+  uint32_t a[4], b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t e0 = fp4_pair_f16<kSel>(w[2 * i]), e1 = fp4_pair_f16<kSel>(w[2 * i + 1]);
+    a[i] = __builtin_bit_cast(uint32_t, (half2_t)(__builtin_bit_cast(half2_t, __builtin_amdgcn_perm(e1, e0, 0x05040100u)) * sc[i]));
+    b[i] = __builtin_bit_cast(uint32_t, (half2_t)(__builtin_bit_cast(half2_t, __builtin_amdgcn_perm(e1, e0, 0x07060302u)) * sc[i]));
+  }
+  __builtin_memcpy(&lo, a, 16);
+  __builtin_memcpy(&hi, b, 16);
+}
+
+// Bytes 2 i, 2 i + 1 of a dword of E4M3 scales -> fp16 pair s_b * 2^-8.
+__device__ __forceinline__ half2_t scale_two(uint32_t four, int i) {
+  return __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0u, four, i ? 0x0C030C02u : 0x0C010C00u) << 7);
+}
+
+template <int D, int MT>
+__global__ __launch_bounds__(256) void k_attn_rows(AttnParams p, RowsPlan plan) {
+  constexpr int kRows = 16 * MT, kTiles = D / 16, kSteps = D / 32;
+  constexpr int kPitch = D + 4;  // floats; 16-byte rows shifted over the banks
+  __shared__ float s_o[2][kRows * kPitch];
+  __shared__ float s_m[4][kRows], s_l[4][kRows];
+  __shared__ uint32_t s_flag;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int n = lane & 15, q = lane >> 4;
+  if (blockIdx.x == gridDim.x - 1) {  // one more workgroup than pieces
+    check_batch(p, &s_flag);
+    return;
+  }
+  const int kvh = blockIdx.x % p.c.H, item = blockIdx.x / p.c.H;
+  Piece pc;
+  if (!find_piece(p, plan, item, pc)) return;
+  const Seq s = load_seq(p, pc.b);
+  const Range range = key_range(p, s);
+  const int u_begin = (int)((int64_t)pc.index * pc.units / pc.count);
+  const int u_end = (int)((int64_t)(pc.index + 1) * pc.units / pc.count);
+  if (pc.index == 0 && kvh == 0 && threadIdx.x == 0) {
+    plan.seq[2 * pc.b] = item;
+    plan.seq[2 * pc.b + 1] = pc.count;
+  }
+  const int rows = s.n * p.g;
+  const int32_t* table = p.table + pc.b * p.table_ld;
+
+  // Q in fp16 under a power of two per row that brings its largest magnitude
+  // to 2^14 .. 2^15: bf16's 8 bits are kept down to 2^-38 of it.
+  half8_t qf[MT][kSteps];
+  float cq[MT];
+  int see_lo[MT], see_hi[MT];
+  const float c0 = p.scale_log2 * *p.c.k_st;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int r = 16 * mt + n, i = r / p.g, h = kvh * p.g + (r - i * p.g);
+    const bool live = r < rows;
+    uint32_t w[kSteps][4];
+    uint32_t top = 0;
+    const uint16_t* at = p.q + (s.row0 + (live ? i : 0)) * p.q_ld_t + (live ? h : 0) * p.q_ld_h + q * (D / 4);
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      const uint4 x = *reinterpret_cast<const uint4*>(at + 8 * u);
+      w[u][0] = live ? x.x : 0u, w[u][1] = live ? x.y : 0u, w[u][2] = live ? x.z : 0u, w[u][3] = live ? x.w : 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max(top, max(w[u][j] << 16 & 0x7FFF0000u, w[u][j] & 0x7FFF0000u));
+    }
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+    const int ex = (int)(top >> 23);
+    const int shift = (top == 0u || ex == 255) ? 0 : 14 + 127 - max(ex, 1);
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        qf[mt][u][2 * j] = (_Float16)__builtin_ldexpf(bf16_lo(w[u][j]), shift);
+        qf[mt][u][2 * j + 1] = (_Float16)__builtin_ldexpf(bf16_hi(w[u][j]), shift);
+      }
+    cq[mt] = __builtin_ldexpf(c0, -shift);
+    int64_t lo, hi;
+    visible(p, s, s.pos0 + i, lo, hi);
+    see_lo[mt] = (int)min<int64_t>(lo, INT32_MAX);
+    see_hi[mt] = live ? (int)max<int64_t>(hi, 0) : 0;
+  }
+  // every row sees all of [all_lo, all_hi)
+  int64_t all_lo, all_hi, x64;
+  visible(p, s, s.pos0, x64, all_hi);
+  visible(p, s, s.pos0 + s.n - 1, all_lo, x64);
+
+  floatx4_t o[MT][kTiles];
+  float ref[MT], ref_safe[MT], l[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    ref[mt] = -INFINITY, ref_safe[mt] = 0.0f, l[mt] = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kTiles; ++u) o[mt][u] = (floatx4_t)(0.0f);
+  }
+
+  // Page ids of the wave's next 32 steps, one load: lane 2 i + t has those of
+  // step i's half t (-1: no key, or an id outside the cache).
+  int ids = -1, ids_at = u_begin;
+  auto fetch_ids = [&](int u0) {
+    const int64_t key = range.base + (int64_t)(u0 + (lane >> 1)) * kUnit + 32 * wave + 16 * (lane & 1);
+    int id = key < range.hi ? table[key >> p.c.log_ps] : -1;
+    if (id >= p.c.num_pages) id = -1;
+    ids = id;
+    ids_at = u0;
+  };
+  auto page_pair = [&](int u, int (&id)[2]) {
+    if (u - ids_at >= 32) fetch_ids(u);
+    id[0] = __builtin_amdgcn_readlane(ids, 2 * (u - ids_at));
+    id[1] = __builtin_amdgcn_readlane(ids, 2 * (u - ids_at) + 1);
+  };
+
+  StepRegs<D> cur, nxt;
+  int id_cur[2], id_nxt[2];
+  fetch_ids(u_begin);
+  page_pair(u_begin, id_cur);
+  const int64_t base = range.base + 32 * wave;
+  load_step<D>(p, cur, id_cur, kvh, (int)((base + (int64_t)u_begin * kUnit) & (p.c.ps - 1)), lane);
+#pragma unroll 1
+  for (int u = u_begin; u < u_end; ++u) {
+    const int64_t kb = base + (int64_t)u * kUnit;
+    if (u + 1 < u_end) {
+      page_pair(u + 1, id_nxt);
+      load_step<D>(p, nxt, id_nxt, kvh, (int)((kb + kUnit) & (p.c.ps - 1)), lane);
+    }
+    if (kb < range.hi) {
+      floatx4_t sc[MT][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t ks = cur.ks[t] & 0x7F7F7F7Fu;  // finite for any byte
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) sc[mt][t] = (floatx4_t)(0.0f);
+#pragma unroll
+        for (int w = 0; w < kSteps; ++w) {
+          const half8_t a = dequant8(cur.k[t][w], scale_pair(ks, w >> 1));
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            sc[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qf[mt][w], sc[mt][t], 0, 0, 0);
+        }
+      }
+      const bool whole = kb >= all_lo && kb + 32 <= all_hi && id_cur[0] >= 0 && id_cur[1] >= 0;
+      half8_t pf[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            float x = sc[mt][t][v] * cq[mt];
+            if (!whole) {
+              const int key = (int)kb + 16 * t + 4 * q + v;
+              x = (key >= see_lo[mt] && key < see_hi[mt] && id_cur[t] >= 0) ? x : -INFINITY;
+            }
+            sc[mt][t][v] = x;
+            top = fmaxf(top, x);
+          }
+        if (__ballot(top > ref[mt] + kRefRoom)) {
+          top = fmaxf(top, __shfl_xor(top, 16, 64));
+          top = fmaxf(top, __shfl_xor(top, 32, 64));
+          const float moved = top > ref[mt] + kRefRoom ? top - kRefStart : ref[mt];
+          const float keep = moved == ref[mt] ? 1.0f : __builtin_amdgcn_exp2f(ref[mt] - moved);
+          ref[mt] = moved;
+          ref_safe[mt] = moved == -INFINITY ? 0.0f : moved;
+          l[mt] *= keep;
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) o[mt][i] *= keep;
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float w = __builtin_amdgcn_exp2f(sc[mt][t][v] - ref_safe[mt]);
+            l[mt] += w;
+            pf[mt][4 * t + v] = (_Float16)w;
+          }
+      }
+      half2_t vs[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) vs[i] = scale_two(cur.vs[i >> 1] & 0x7F7F7F7Fu, i & 1);
+#pragma unroll
+      for (int j = 0; j < StepRegs<D>::kVW; ++j) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = cur.v[i][j];
+        half8_t a[8];
+        v_operands<0>(w, vs, a[0], a[1]);
+        v_operands<1>(w, vs, a[2], a[3]);
+        if constexpr (D > 64) {
+          v_operands<2>(w, vs, a[4], a[5]);
+          v_operands<3>(w, vs, a[6], a[7]);
+        }
+#pragma unroll
+        for (int e = 0; e < (D > 64 ? 8 : 4); ++e)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            o[mt][8 * j + e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[e], pf[mt], o[mt][8 * j + e], 0, 0, 0);
+      }
+    }
+    cur = nxt;
+    id_cur[0] = id_nxt[0], id_cur[1] = id_nxt[1];
+  }
+
+  // Join the four waves: each scales its part to the common reference, waves
+  // 2 and 3 hand theirs over through LDS, waves 0 and 1 add and leave two
+  // parts for the workgroup.
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    l[mt] += __shfl_xor(l[mt], 16, 64);
+    l[mt] += __shfl_xor(l[mt], 32, 64);
+    if (q == 0) s_m[wave][16 * mt + n] = ref[mt], s_l[wave][16 * mt + n] = l[mt];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int r = 16 * mt + n;
+    const float m = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+    const float f = ref[mt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ref[mt] - m);
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) o[mt][i] *= f;
+  }
+  float* part = s_o[wave & 1];
+  auto each = [&](auto&& f) {  // float4 of 4 consecutive elements of the lane's row
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int i = 0; i < kTiles / 4; ++i)
+          f(reinterpret_cast<float4*>(part + (16 * mt + n) * kPitch + (4 * q + v) * kTiles + 4 * i),
+            make_float4(o[mt][4 * i][v], o[mt][4 * i + 1][v], o[mt][4 * i + 2][v], o[mt][4 * i + 3][v]));
+  };
+  if (wave >= 2) each([](float4* at, float4 x) { *at = x; });
+  __syncthreads();
+  if (wave < 2)
+    each([](float4* at, float4 x) {
+      const float4 y = *at;
+      *at = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    });
+  __syncthreads();
+  const float v_st = *p.c.v_st;
+  constexpr int kChunks = D / 8;
+  for (int e = threadIdx.x; e < kRows * kChunks; e += 256) {
+    const int r = e / kChunks, ch = e - r * kChunks;
+    if (r >= rows) break;
+    const float m = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      sum += s_m[w][r] == -INFINITY ? 0.0f : s_l[w][r] * __builtin_amdgcn_exp2f(s_m[w][r] - m);
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 a = *reinterpret_cast<const float4*>(s_o[0] + r * kPitch + 8 * ch + 4 * i);
+      const float4 b = *reinterpret_cast<const float4*>(s_o[1] + r * kPitch + 8 * ch + 4 * i);
+      x[4 * i] = a.x + b.x, x[4 * i + 1] = a.y + b.y, x[4 * i + 2] = a.z + b.z, x[4 * i + 3] = a.w + b.w;
+    }
+    if (pc.count == 1) {
+      const int i = r / p.g, h = kvh * p.g + (r - i * p.g);
+      const float inv = sum == 0.0f ? 0.0f : v_st / sum;
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = f32_to_bf16_any(x[2 * j] * inv) | (f32_to_bf16_any(x[2 * j + 1] * inv) << 16);
+      *reinterpret_cast<uint4*>(p.out + (s.row0 + i) * p.out_ld_t + h * p.out_ld_h + 8 * ch) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+      if (p.lse && ch == 0)
+        p.lse[(int64_t)(s.row0 + i) * p.Hq + h] = sum == 0.0f ? -INFINITY : (m + __builtin_log2f(sum)) * kLn2;
+    } else {
+      const int64_t slot = (int64_t)blockIdx.x * kRows + r;
+      float4* at = reinterpret_cast<float4*>(plan.part_o + slot * D + 8 * ch);
+      at[0] = make_float4(x[0], x[1], x[2], x[3]);
+      at[1] = make_float4(x[4], x[5], x[6], x[7]);
+      if (ch == 0) plan.part_ml[slot] = make_float2(m, sum);
+    }
+  }
+}
+
+// Joins the pieces of a split sequence: a workgroup per row and key/value
+// head, its four waves taking pieces in turn, a lane D / 64 elements.
+template <int D, int kRows>
+__global__ __launch_bounds__(256) void k_attn_rows_join(AttnParams p, RowsPlan plan) {
+  constexpr int kE = D / 64;
+  __shared__ float s_o[4][D];
+  __shared__ float s_l[4], s_m[4];
+  const int b = blockIdx.x, kvh = blockIdx.y, r = blockIdx.z;
+  const Seq s = load_seq(p, b);
+  if (r >= s.n * p.g || s.n * p.g > plan.max_rows) return;
+  const int item = plan.seq[2 * b], count = plan.seq[2 * b + 1];
+  if (count == 1) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  auto slot = [&](int i) { return ((int64_t)(item + i) * p.c.H + kvh) * kRows + r; };
+  float m = -INFINITY;
+  for (int i = threadIdx.x; i < count; i += 256) m = fmaxf(m, plan.part_ml[slot(i)].x);
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x, 64));
+  if (lane == 0) s_m[wave] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  const float ref = m == -INFINITY ? 0.0f : m;
+  float o[kE], l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) o[e] = 0.0f;
+#pragma unroll 8
+  for (int i = wave; i < count; i += 4) {
+    const int64_t at = slot(i);
+    const float2 ml = plan.part_ml[at];
+    const float f = __builtin_amdgcn_exp2f(ml.x - ref);
+    l += ml.y * f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] += plan.part_o[at * D + kE * lane + e] * f;
+  }
+#pragma unroll
+  for (int e = 0; e < kE; ++e) s_o[wave][kE * lane + e] = o[e];
+  if (lane == 0) s_l[wave] = l;
+  __syncthreads();
+  const float sum = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+  const int i = r / p.g, h = kvh * p.g + (r - i * p.g);
+  const float inv = sum == 0.0f ? 0.0f : *p.c.v_st / sum;
+  for (int d = threadIdx.x; d < D; d += 256)
+    p.out[(s.row0 + i) * p.out_ld_t + h * p.out_ld_h + d] =
+        (uint16_t)f32_to_bf16_any((s_o[0][d] + s_o[1][d] + s_o[2][d] + s_o[3][d]) * inv);
+  if (p.lse && threadIdx.x == 0)
+    p.lse[(int64_t)(s.row0 + i) * p.Hq + h] = sum == 0.0f ? -INFINITY : (m + __builtin_log2f(sum)) * kLn2;
+}
+
+template <int D, int MT>
+int launch_rows(const AttnParams& p, const RowsPlan& plan, hipStream_t s) {
+  hipLaunchKernelGGL((k_attn_rows<D, MT>), dim3((unsigned)(plan.items * p.c.H + 1)), dim3(256), 0, s, p, plan);
+  if (int rc = last_launch()) return rc;
+  if (!plan.may_split) return NVQ_OK;
+  const int rows = std::min<int64_t>((int64_t)p.max_q * p.g, 16 * MT);
+  hipLaunchKernelGGL((k_attn_rows_join<D, 16 * MT>), dim3((unsigned)p.B, (unsigned)p.c.H, (unsigned)rows), dim3(256),
+                     0, s, p, plan);
+  return last_launch();
+}
+
+}  // namespace
+
+// Row tiles of 16 that the kernel takes for sequences of up to `rows` rows per
+// key/value head; 0: none.
+int attn_rows_tiles(int D, int64_t rows) {
+  if (D != 64 && D != 128 && D != 256) return 0;
+  return rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
+}
+
+void attn_rows_plan(const AttnParams& p, int tiles, WsCarve& ws, RowsPlan& plan) {
+  plan.max_rows = 16 * tiles;
+  plan.min_units = kRowsMinUnits;
+  plan.target = kRowsTarget;
+  const int64_t units = (p.num_keys + 31 + kUnit - 1) / kUnit;  // most of a sequence
+  plan.may_split = units > plan.min_units;
+  // pieces: ceil(units / per) each, per >= total H / target and >= min_units
+  const int64_t by_target = (plan.target + p.c.H - 1) / p.c.H + p.B;
+  const int64_t by_units = p.B * std::max<int64_t>(1, (units + plan.min_units - 1) / plan.min_units);
+  plan.items = std::min(by_target, by_units);
+  plan.seq = ws.take<int32_t>(2 * (size_t)p.B);
+  const size_t slots = plan.may_split ? (size_t)(plan.items * p.c.H) * plan.max_rows : 0;
+  plan.part_ml = ws.take<float2>(slots);
+  plan.part_o = ws.take<float>(slots * p.c.D);
+}
+
+int attn_rows_launch(const AttnParams& p, int tiles, const RowsPlan& plan, hipStream_t s) {
+  switch (p.c.D * 4 + tiles) {
+    case 64 * 4 + 1: return launch_rows<64, 1>(p, plan, s);
+    case 64 * 4 + 2: return launch_rows<64, 2>(p, plan, s);
+    case 128 * 4 + 1: return launch_rows<128, 1>(p, plan, s);
+    case 128 * 4 + 2: return launch_rows<128, 2>(p, plan, s);
+    case 256 * 4 + 1: return launch_rows<256, 1>(p, plan, s);
+    default: return launch_rows<256, 2>(p, plan, s);
+  }
+}
+
+}  // namespace nvq

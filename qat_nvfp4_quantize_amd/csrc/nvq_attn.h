@@ -1,0 +1,98 @@
+// What the attention kernels share: the call's parameters, the sequences as
+// the device sees them and the check of the index arrays.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "nvq.h"
+#include "nvq_kv.h"
+
+namespace nvq {
+
+struct AttnParams {
+  KvPages c;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  const int32_t *cu_q, *kv_len, *table;
+  int64_t q_ld_t, q_ld_h, out_ld_t, out_ld_h, table_ld;
+  int64_t window;    // 0: none
+  int64_t num_keys;  // keys a row of the block table covers
+  int total_q, B, max_q, Hq, g;
+  int causal;
+  float scale_log2;  // softmax_scale * log2(e)
+  uint32_t* status;
+};
+
+// Plan of the few-rows kernel, and where the pieces of split sequences go.
+struct RowsPlan {
+  int max_rows;   // sequences with more rows per key/value head are left out
+  int min_units;  // smallest piece, in 128-key units
+  int target;     // pieces times heads aimed at
+  int may_split;
+  int64_t items;     // most pieces there can be
+  int32_t* seq;      // [B][2] first piece and their number
+  float2* part_ml;   // [piece][head][max_rows] reference and sum
+  float* part_o;     // [piece][head][max_rows][D]
+};
+constexpr int kRowsMinUnits = 2;
+constexpr int kRowsTarget = 1024;
+
+int attn_rows_tiles(int D, int64_t rows);
+void attn_rows_plan(const AttnParams& p, int tiles, WsCarve& ws, RowsPlan& plan);
+int attn_rows_launch(const AttnParams& p, int tiles, const RowsPlan& plan, hipStream_t s);
+
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// Rows and keys of sequence b, cut to what the call's buffers hold.
+struct Seq {
+  int row0, n;   // query rows
+  int64_t len;   // keys
+  int64_t pos0;  // position of the first row: the rows are the last positions
+};
+__device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
+  Seq s;
+  s.row0 = min(max(p.cu_q[b], 0), p.total_q);
+  const int n = max(min(p.cu_q[b + 1], p.total_q) - s.row0, 0);
+  s.n = min(n, p.max_q);
+  s.len = max(p.kv_len[b], 0);
+  s.pos0 = s.len - n;
+  return s;
+}
+
+// Visible keys [lo, hi) of the query at position pos.
+__device__ __forceinline__ void visible(const AttnParams& p, const Seq& s, int64_t pos, int64_t& lo, int64_t& hi) {
+  hi = min(p.causal ? pos + 1 : s.len, min(s.len, p.num_keys));
+  lo = p.window > 0 ? max<int64_t>(pos - p.window + 1, 0) : 0;
+}
+
+// One workgroup looks over the index arrays and writes the status word:
+// lengths and row ranges of every sequence, and the page id of every page
+// that some query row of it can see.  It runs beside the others, which only
+// stay inside the buffers, so no atomic and no clearing is needed.
+__device__ __forceinline__ void check_batch(const AttnParams& p, uint32_t* s_flag) {
+  if (threadIdx.x == 0) *s_flag = 0u;
+  __syncthreads();
+  bool bad = false;
+  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+    const int64_t r0 = p.cu_q[b], r1 = p.cu_q[b + 1], len = p.kv_len[b];
+    bad |= r0 < 0 || r1 < r0 || r1 > p.total_q || r1 - r0 > p.max_q || len < 0 || (r1 > r0 && len > p.num_keys);
+  }
+  for (int b = 0; b < p.B; ++b) {
+    const Seq s = load_seq(p, b);
+    if (s.n == 0) continue;
+    int64_t lo, hi, x;
+    visible(p, s, s.pos0, lo, x);
+    visible(p, s, s.len - 1, x, hi);
+    for (int64_t i = (lo >> p.c.log_ps) + threadIdx.x; (i << p.c.log_ps) < hi; i += blockDim.x) {
+      const int32_t id = p.table[b * p.table_ld + i];
+      bad |= id < 0 || id >= p.c.num_pages;
+    }
+  }
+  if (bad) atomicOr(s_flag, (uint32_t)NVQ_STATUS_BAD_SEQUENCE);
+  __syncthreads();
+  if (threadIdx.x == 0) *p.status = *s_flag;
+}
+
+}  // namespace nvq
