@@ -562,8 +562,8 @@ typedef struct nvq_paged_attention_args {
  * B, max_q, q_heads, table_width and the cache's heads, head_dim, page_size). */
 size_t nvq_paged_attention_workspace_bytes(const nvq_kv_cache* cache,
                                            const nvq_paged_attention_args* args);
-/* Limits: total_q < 2^24, q_heads <= 32768, B <= 65535, B * heads <= 2^22,
- * table_width * page_size <= INT32_MAX.
+/* Limits: total_q < 2^24, q_heads <= 32768, total_q * q_heads <= 2^30, B <=
+ * 65535, B * heads <= 2^22, table_width * page_size <= INT32_MAX.
  * Errors: NVQ_EINVAL, NVQ_ESHAPE, NVQ_EALIGN, NVQ_EWORKSPACE; nothing is
  * launched then. */
 int nvq_paged_attention(const nvq_kv_cache* cache, const nvq_paged_attention_args* args,

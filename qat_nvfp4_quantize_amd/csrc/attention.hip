@@ -150,7 +150,9 @@ int attn_sizes(const nvq_kv_cache* cache, const nvq_paged_attention_args* a, Att
   if (cache->heads < 1 || ps < 16 || ps > 65536 || a->q_heads < 1 || a->q_heads > 32768 ||
       a->q_heads % cache->heads)
     return NVQ_ESHAPE;
-  if (a->table_width > INT32_MAX / ps || a->B * cache->heads > (1 << 22)) return NVQ_ESHAPE;
+  if (a->table_width > INT32_MAX / ps || a->B * cache->heads > (1 << 22) ||
+      a->total_q * a->q_heads > (1 << 30))
+    return NVQ_ESHAPE;
   p.total_q = (int)a->total_q, p.B = (int)a->B;
   p.max_q = (int)(a->max_q == 0 ? a->total_q : std::min(a->max_q, a->total_q));
   p.Hq = a->q_heads, p.g = a->q_heads / cache->heads;
@@ -159,12 +161,32 @@ int attn_sizes(const nvq_kv_cache* cache, const nvq_paged_attention_args* a, Att
   return NVQ_OK;
 }
 
-// Lays the workspace out; returns its bytes.
-size_t attn_plan(const AttnParams& p, void* ws, RowsPlan& rows) {
+// Which kernels a call takes, and their workspace.  Head dimensions 64, 128
+// and 256 go to the MFMA kernels: sequences of few rows per key/value head to
+// the one that reads the pages into operands, the others to the one that
+// shares dequantized tiles; a batch that may hold both kinds launches both,
+// and each leaves the other's sequences out.  Other dimensions take one
+// workgroup per row.
+struct Plan {
+  RowsPlan rows;
+  ChunkPlan chunk;
+  bool use_rows, use_chunk;
+  size_t bytes;
+};
+
+Plan attn_plan(const AttnParams& p, void* ws) {
+  Plan plan{};
   WsCarve c(ws);
-  rows.max_rows = 0;
-  if (const int tiles = attn_rows_tiles(p.c.D, (int64_t)p.max_q * p.g)) attn_rows_plan(p, tiles, c, rows);
-  return c.off;
+  if (p.c.D == 64 || p.c.D == 128 || p.c.D == 256) {
+    int tiles = attn_rows_tiles((int64_t)p.max_q * p.g);
+    plan.use_chunk = tiles == 0;
+    if (plan.use_chunk && p.B > 1) tiles = attn_rows_tiles(p.g);  // single tokens beside the chunks
+    plan.use_rows = tiles > 0;
+    if (plan.use_rows) attn_rows_plan(p, tiles, c, plan.rows);
+    if (plan.use_chunk) attn_chunk_plan(p, 16 * tiles, !plan.use_rows, c, plan.chunk);
+  }
+  plan.bytes = c.off;
+  return plan;
 }
 
 }  // namespace
@@ -176,8 +198,7 @@ extern "C" size_t nvq_paged_attention_workspace_bytes(const nvq_kv_cache* cache,
                                                       const nvq_paged_attention_args* args) {
   AttnParams p{};
   if (attn_sizes(cache, args, p)) return kAlign;
-  RowsPlan rows;
-  return attn_plan(p, nullptr, rows);
+  return attn_plan(p, nullptr).bytes;
 }
 
 extern "C" int nvq_paged_attention(const nvq_kv_cache* cache, const nvq_paged_attention_args* args, void* stream) {
@@ -206,8 +227,8 @@ extern "C" int nvq_paged_attention(const nvq_kv_cache* cache, const nvq_paged_at
     return NVQ_EALIGN;
   if (!a.ws) return NVQ_EINVAL;
   if (!aligned256(a.ws)) return NVQ_EALIGN;
-  RowsPlan rows;
-  if (a.ws_bytes < attn_plan(p, a.ws, rows)) return NVQ_EWORKSPACE;
+  const Plan plan = attn_plan(p, a.ws);
+  if (a.ws_bytes < plan.bytes) return NVQ_EWORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   p.status = static_cast<uint32_t*>(a.ws);
   if (p.total_q == 0 || p.B == 0) return clear_status(p.status, s);
@@ -216,7 +237,10 @@ extern "C" int nvq_paged_attention(const nvq_kv_cache* cache, const nvq_paged_at
   p.cu_q = a.cu_q, p.kv_len = a.kv_len, p.table = a.block_table;
   p.window = a.window, p.causal = a.causal;
   p.scale_log2 = a.softmax_scale * 1.44269504088896340736f;
-  if (rows.max_rows) return attn_rows_launch(p, rows.max_rows / 16, rows, s);
+  if (plan.use_rows)
+    if (int rc = attn_rows_launch(p, plan.rows, s)) return rc;
+  if (plan.use_chunk) return attn_chunk_launch(p, plan.chunk, s);
+  if (plan.use_rows) return NVQ_OK;
   hipLaunchKernelGGL(k_attn_any, dim3((unsigned)p.total_q, (unsigned)p.Hq + 1), dim3(256), 0, s, p);
   return last_launch();
 }

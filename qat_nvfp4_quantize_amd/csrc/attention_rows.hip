@@ -509,10 +509,7 @@ int launch_rows(const AttnParams& p, const RowsPlan& plan, hipStream_t s) {
 
 // Row tiles of 16 that the kernel takes for sequences of up to `rows` rows per
 // key/value head; 0: none.
-int attn_rows_tiles(int D, int64_t rows) {
-  if (D != 64 && D != 128 && D != 256) return 0;
-  return rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
-}
+int attn_rows_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 0; }
 
 void attn_rows_plan(const AttnParams& p, int tiles, WsCarve& ws, RowsPlan& plan) {
   plan.max_rows = 16 * tiles;
@@ -530,8 +527,8 @@ void attn_rows_plan(const AttnParams& p, int tiles, WsCarve& ws, RowsPlan& plan)
   plan.part_o = ws.take<float>(slots * p.c.D);
 }
 
-int attn_rows_launch(const AttnParams& p, int tiles, const RowsPlan& plan, hipStream_t s) {
-  switch (p.c.D * 4 + tiles) {
+int attn_rows_launch(const AttnParams& p, const RowsPlan& plan, hipStream_t s) {
+  switch (p.c.D * 4 + plan.max_rows / 16) {
     case 64 * 4 + 1: return launch_rows<64, 1>(p, plan, s);
     case 64 * 4 + 2: return launch_rows<64, 2>(p, plan, s);
     case 128 * 4 + 1: return launch_rows<128, 1>(p, plan, s);

@@ -46,7 +46,12 @@ def attention(q, keys, values, first, scale, causal, window):
     of D products, U32 D sum |q k| scale at most, plus a few roundings of the
     score itself (8 U32 |s| with the reference's subtraction and the base-2
     exponential).  The sums over the L keys add 2 L U32 A, and a rescaling or a
-    joint a few more roundings."""
+    joint a few more roundings.  FP16 is relative only for normal numbers: a
+    weight under 2^-14 is rounded to a multiple of 2^-24, so it is off by 2^-25
+    at most; the largest weight is at least 2^9 (the running reference is set 9
+    below a new maximum and never lies nearer to it), so the sum of weights is
+    too, and such a key moves out by 2^-34 |v|: 2^-34 sum |v| in all, which A
+    does not cover where the keys of large weight have v = 0."""
     n, Hq, D = q.shape
     L, Hkv, _ = keys.shape
     g = Hq // Hkv
@@ -72,6 +77,7 @@ def attention(q, keys, values, first, scale, causal, window):
             absum = (np.abs(k) @ np.abs(q[i, h])).max() * abs(scale)
             d = U32 * (D * absum + 8 * np.abs(s).max())
             tol[i, h] = BF16 * np.abs(out[i, h]) + A * (FP16 + 2 * d + 2 * len(s) * U32 + 64 * U32)
+            tol[i, h] += 2.0 ** -34 * np.abs(v).sum(0)
     return out, lse, tol
 
 
