@@ -32,12 +32,12 @@ __global__ __launch_bounds__(256) void k_attn_any(AttnParams p) {
   __shared__ float s_q[kAnyMaxD];
   __shared__ float s_o[4][kAnyMaxD];
   __shared__ float s_ml[4][2];
-  __shared__ uint32_t s_flag;
-  if (blockIdx.y == (unsigned)p.Hq) {
-    if (blockIdx.x == 0) check_batch(p, &s_flag);
+  __shared__ CheckLds s_check;
+  if (blockIdx.y == 0) {
+    if (blockIdx.x == 0) check_batch(p, s_check);
     return;
   }
-  const int row = blockIdx.x, h = blockIdx.y, kvh = h / p.g;
+  const int row = blockIdx.x, h = blockIdx.y - 1, kvh = h / p.g;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int D = p.c.D, nb = D >> 4;
   // the last sequence that starts at or before the row

@@ -206,11 +206,11 @@ template <int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams p, ChunkPlan plan) {
   constexpr int kPitch = ChunkLds<D>::kPitch, kSteps = D / 16, kOut = D / 32;
   __shared__ ChunkLds<D> lds;
-  if (plan.check && blockIdx.x == gridDim.x - 1) {
-    check_batch(p, &lds.dead[0][0]);
+  if (plan.check && blockIdx.x == 0) {
+    check_batch(p, reinterpret_cast<CheckLds&>(lds));
     return;
   }
-  const int kvh = blockIdx.x % p.c.H, item = blockIdx.x / p.c.H;
+  const int block = blockIdx.x - plan.check, kvh = block % p.c.H, item = block / p.c.H;
   if (item >= plan.count[0]) return;
   const int4 it = plan.item[item];
   const int b = __builtin_amdgcn_readfirstlane(it.x), qt = __builtin_amdgcn_readfirstlane(it.y);

@@ -116,48 +116,53 @@ struct StepRegs {
   uint32_t k[2][kKW], ks[2], v[8][kVW], vs[2];
 };
 
+// Bases are wave-uniform (the page ids come from a readlane) and a lane's
+// offsets inside a 16-key group never change, so the loads need no address
+// arithmetic in vector registers.
 template <int D>
 __device__ __forceinline__ void load_step(const AttnParams& p, StepRegs<D>& r, const int (&id)[2], int kvh, int off0,
                                           int lane) {
-  const int n = lane & 15, q = lane >> 4;
+  const uint32_t n = lane & 15, q = lane >> 4;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int64_t tile = ((int64_t)max(id[t], 0) * p.c.H + kvh) << p.c.log_ps;  // a masked page reads page 0
     const int off = (off0 + 16 * t) & (p.c.ps - 1);
-    const uint8_t* kc = p.c.k_codes + (tile + off) * (D / 2) + n * (D / 2) + q * (D / 8);
+    const uint8_t* kc = p.c.k_codes + (tile + off) * (D / 2);
+    const uint32_t kl = n * (D / 2) + q * (D / 8);
     if constexpr (D == 64) {
-      const uint2 w = *reinterpret_cast<const uint2*>(kc);
+      const uint2 w = *reinterpret_cast<const uint2*>(kc + kl);
       r.k[t][0] = w.x, r.k[t][1] = w.y;
     } else {
 #pragma unroll
       for (int i = 0; i < D / 128; ++i) {
-        const uint4 w = reinterpret_cast<const uint4*>(kc)[i];
+        const uint4 w = *reinterpret_cast<const uint4*>(kc + kl + 16 * i);
         r.k[t][4 * i] = w.x, r.k[t][4 * i + 1] = w.y, r.k[t][4 * i + 2] = w.z, r.k[t][4 * i + 3] = w.w;
       }
     }
-    const uint8_t* ks = p.c.k_scales + (tile + off) * (D / 16) + n * (D / 16) + q * (D / 64);
+    const uint8_t* ks = p.c.k_scales + (tile + off) * (D / 16);
+    const uint32_t sl = n * (D / 16) + q * (D / 64);
     if constexpr (D == 64)
-      r.ks[t] = *ks;
+      r.ks[t] = ks[sl];
     else if constexpr (D == 128)
-      r.ks[t] = *reinterpret_cast<const uint16_t*>(ks);
+      r.ks[t] = *reinterpret_cast<const uint16_t*>(ks + sl);
     else
-      r.ks[t] = *reinterpret_cast<const uint32_t*>(ks);
-    const uint8_t* vc = p.c.v_codes + (tile + off + 4 * q) * (D / 2) + n * (D / 32);
+      r.ks[t] = *reinterpret_cast<const uint32_t*>(ks + sl);
+    const uint8_t* vc = p.c.v_codes + (tile + off) * (D / 2);
+    const uint32_t vl = 4 * q * (D / 2) + n * (D / 32);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint8_t* at = vc + i * (D / 2);
       uint32_t(&w)[StepRegs<D>::kVW] = r.v[4 * t + i];
       if constexpr (D == 64) {
-        w[0] = *reinterpret_cast<const uint16_t*>(at);
+        w[0] = *reinterpret_cast<const uint16_t*>(vc + vl + i * (D / 2));
       } else if constexpr (D == 128) {
-        w[0] = *reinterpret_cast<const uint32_t*>(at);
+        w[0] = *reinterpret_cast<const uint32_t*>(vc + vl + i * (D / 2));
       } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(at);
+        const uint2 x = *reinterpret_cast<const uint2*>(vc + vl + i * (D / 2));
         w[0] = x.x, w[1] = x.y;
       }
     }
-    r.vs[t] = *reinterpret_cast<const uint32_t*>(p.c.v_scales + tile * (D / 16) + ((int64_t)(n * D / 256) << p.c.log_ps) +
-                                                 off + 4 * q);
+    const uint8_t* vs = p.c.v_scales + tile * (D / 16) + off;
+    r.vs[t] = *reinterpret_cast<const uint32_t*>(vs + ((n * D / 256) << p.c.log_ps) + 4 * q);
   }
 }
 
@@ -187,19 +192,19 @@ __device__ __forceinline__ half2_t scale_two(uint32_t four, int i) {
 }
 
 template <int D, int MT>
-__global__ __launch_bounds__(256) void k_attn_rows(AttnParams p, RowsPlan plan) {
+__global__ __launch_bounds__(256, D * MT > 256 ? 1 : 2) void k_attn_rows(AttnParams p, RowsPlan plan) {
   constexpr int kRows = 16 * MT, kTiles = D / 16, kSteps = D / 32;
   constexpr int kPitch = D + 4;  // floats; 16-byte rows shifted over the banks
   __shared__ float s_o[2][kRows * kPitch];
   __shared__ float s_m[4][kRows], s_l[4][kRows];
-  __shared__ uint32_t s_flag;
+  __shared__ CheckLds s_check;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int n = lane & 15, q = lane >> 4;
-  if (blockIdx.x == gridDim.x - 1) {  // one more workgroup than pieces
-    check_batch(p, &s_flag);
+  if (blockIdx.x == 0) {  // one workgroup more than pieces
+    check_batch(p, s_check);
     return;
   }
-  const int kvh = blockIdx.x % p.c.H, item = blockIdx.x / p.c.H;
+  const int block = blockIdx.x - 1, kvh = block % p.c.H, item = block / p.c.H;
   Piece pc;
   if (!find_piece(p, plan, item, pc)) return;
   const Seq s = load_seq(p, pc.b);
@@ -280,19 +285,13 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnParams p, RowsPlan plan) 
     id[1] = __builtin_amdgcn_readlane(ids, 2 * (u - ids_at) + 1);
   };
 
-  StepRegs<D> cur, nxt;
-  int id_cur[2], id_nxt[2];
-  fetch_ids(u_begin);
-  page_pair(u_begin, id_cur);
   const int64_t base = range.base + 32 * wave;
-  load_step<D>(p, cur, id_cur, kvh, (int)((base + (int64_t)u_begin * kUnit) & (p.c.ps - 1)), lane);
-#pragma unroll 1
-  for (int u = u_begin; u < u_end; ++u) {
+  auto fetch = [&](StepRegs<D>& regs, int (&id)[2], int u) {
+    page_pair(u, id);
+    load_step<D>(p, regs, id, kvh, (int)((base + (int64_t)u * kUnit) & (p.c.ps - 1)), lane);
+  };
+  auto consume = [&](const StepRegs<D>& cur, const int (&id)[2], int u) {
     const int64_t kb = base + (int64_t)u * kUnit;
-    if (u + 1 < u_end) {
-      page_pair(u + 1, id_nxt);
-      load_step<D>(p, nxt, id_nxt, kvh, (int)((kb + kUnit) & (p.c.ps - 1)), lane);
-    }
     if (kb < range.hi) {
       floatx4_t sc[MT][2];
 #pragma unroll
@@ -308,7 +307,7 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnParams p, RowsPlan plan) 
             sc[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qf[mt][w], sc[mt][t], 0, 0, 0);
         }
       }
-      const bool whole = kb >= all_lo && kb + 32 <= all_hi && id_cur[0] >= 0 && id_cur[1] >= 0;
+      const bool whole = kb >= all_lo && kb + 32 <= all_hi && id[0] >= 0 && id[1] >= 0;
       half8_t pf[MT];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -320,7 +319,7 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnParams p, RowsPlan plan) 
             float x = sc[mt][t][v] * cq[mt];
             if (!whole) {
               const int key = (int)kb + 16 * t + 4 * q + v;
-              x = (key >= see_lo[mt] && key < see_hi[mt] && id_cur[t] >= 0) ? x : -INFINITY;
+              x = (key >= see_lo[mt] && key < see_hi[mt] && id[t] >= 0) ? x : -INFINITY;
             }
             sc[mt][t][v] = x;
             top = fmaxf(top, x);
@@ -367,8 +366,20 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnParams p, RowsPlan plan) 
             o[mt][8 * j + e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[e], pf[mt], o[mt][8 * j + e], 0, 0, 0);
       }
     }
-    cur = nxt;
-    id_cur[0] = id_nxt[0], id_cur[1] = id_nxt[1];
+  };
+  // two register sets in turn: the next step's loads are in flight while a
+  // step is computed, and nothing is copied
+  StepRegs<D> even, odd;
+  int id_even[2], id_odd[2];
+  fetch_ids(u_begin);
+  fetch(even, id_even, u_begin);
+#pragma unroll 1
+  for (int u = u_begin; u < u_end; u += 2) {
+    if (u + 1 < u_end) fetch(odd, id_odd, u + 1);
+    consume(even, id_even, u);
+    if (u + 1 >= u_end) break;
+    if (u + 2 < u_end) fetch(even, id_even, u + 2);
+    consume(odd, id_odd, u + 1);
   }
 
   // Join the four waves: each scales its part to the common reference, waves
@@ -437,7 +448,7 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnParams p, RowsPlan plan) 
       if (p.lse && ch == 0)
         p.lse[(int64_t)(s.row0 + i) * p.Hq + h] = sum == 0.0f ? -INFINITY : (m + __builtin_log2f(sum)) * kLn2;
     } else {
-      const int64_t slot = (int64_t)blockIdx.x * kRows + r;
+      const int64_t slot = (int64_t)block * kRows + r;
       float4* at = reinterpret_cast<float4*>(plan.part_o + slot * D + 8 * ch);
       at[0] = make_float4(x[0], x[1], x[2], x[3]);
       at[1] = make_float4(x[4], x[5], x[6], x[7]);

@@ -524,8 +524,27 @@ def qat_fakequant_gemm_w4a16(mode, w_codes, w_scales, w_tensor_scale, expert_off
 
 
 # ------------------------------------------ rotary positions, paged KV cache --
-def _same_device(dev, **tensors):
-    """Every given tensor lies on the GPU `dev`."""
+# A decode step makes these calls for every layer, and their kernels run for a
+# few microseconds, so the checks below are kept to attribute reads.
+_HEAD_TYPES = (torch.bfloat16, torch.float32)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(fn, name, dev, *args):
+    """Calls the library with `dev` as the current device, on its current stream."""
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc != 0:
+        raise NvqError(name, rc)
+
+
+def _on(dev, **tensors):
+    """Raises for the first tensor that does not lie on the GPU `dev`."""
     for name, t in tensors.items():
         if t is not None and t.device != dev:
             raise ValueError(f"{name} must be a GPU tensor on {dev}, got {t.device}")
@@ -533,47 +552,27 @@ def _same_device(dev, **tensors):
 
 def _typed(t, name, dtype, *shape):
     """A contiguous tensor of this dtype and (where given) shape."""
-    if t.dtype != dtype or not t.is_contiguous() or (shape and tuple(t.shape) != shape):
+    if t.dtype != dtype or not t.is_contiguous() or (shape and t.shape != shape):
         raise ValueError(f"{name} must be contiguous {dtype}" + (f" {list(shape)}" if shape else "")
-                         + f", got {t.dtype} {list(t.shape)}")
-    return t
+                         + f", got {t.dtype} {list(t.shape)}, strides {list(t.stride())}")
 
 
-def _heads(t, name, dtypes):
+def _heads(t, name, dtypes=_HEAD_TYPES):
     """(T, H, D, ld_t, ld_h) of [T, H, D] projected heads with unit element
-    stride, tokens and heads strided freely (a slice of a fused projection)."""
+    stride, tokens and heads strided freely (a slice of a fused projection);
+    a stride of 0 stands for the dense one, also where the axis has one entry."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dim() != 3 or t.dtype not in dtypes:
         raise ValueError(f"{name} must be [T, H, D] of {dtypes}, got {t.dtype} {list(t.shape)}")
     T, H, D = t.shape
+    if t.is_contiguous():
+        return T, H, D, 0, 0
     st, sh, sd = t.stride()
     if (D > 1 and sd != 1) or (T > 1 and st <= 0) or (H > 1 and sh <= 0):
         raise ValueError(f"{name} must have unit element stride and no broadcast axis, got "
                          f"strides {t.stride()}")
-    # the stride of an axis of one is free: 0 stands for the dense one
     return T, H, D, (st if T > 1 else 0), (sh if H > 1 else 0)
-
-
-class _Device:
-    """Makes `dev` the current device for a call, and gives its current stream."""
-
-    def __init__(self, dev):
-        self.dev = dev
-        self.guard = None
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.dev.index:
-            self.guard = torch.cuda.device(self.dev)
-            self.guard.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream(self.dev).cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-_HEAD_TYPES = (torch.bfloat16, torch.float32)
 
 
 def nvq_rope_frequencies(rot_dim, base=10000.0, kind=NVQ_ROPE_PLAIN, factor=1.0, orig_len=0.0,
@@ -592,22 +591,21 @@ def nvq_rope(x, positions, inv_freq, interleaved=False, magnitude=1.0, inverse=F
     2 * len(inv_freq) elements of each head turned by positions [T] int32 times
     inv_freq (fp64, on the GPU); inverse turns back (the gradient).  out: a
     tensor like x to write, x itself for in place."""
-    T, H, D, ld_t, ld_h = _heads(x, "x", _HEAD_TYPES)
+    T, H, D, ld_t, ld_h = _heads(x, "x")
+    dev = x.device
+    old_t = old_h = 0
     if out is None:
-        out = torch.empty(T, H, D, dtype=x.dtype, device=x.device)
-        old_t = old_h = 0
+        out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
     else:
         if out.shape != x.shape or out.dtype != x.dtype:
             raise ValueError("out must have the shape and dtype of x")
-        _, _, _, old_t, old_h = _heads(out, "out", _HEAD_TYPES)
+        _, _, _, old_t, old_h = _heads(out, "out")
     _typed(positions, "positions", torch.int32, T)
     _typed(inv_freq, "inv_freq", torch.float64)
-    _same_device(x.device, positions=positions, inv_freq=inv_freq, out=out)
-    with _Device(x.device) as stream:
-        _check("nvq_rope", load().nvq_rope(
-            x.data_ptr(), _dtype_code(x), T, H, D, ld_t, ld_h, positions.data_ptr(),
-            inv_freq.data_ptr(), 2 * inv_freq.numel(), int(bool(interleaved)), magnitude,
-            int(bool(inverse)), out.data_ptr(), old_t, old_h, stream))
+    _on(dev, positions=positions, inv_freq=inv_freq, out=out)
+    _call((_lib or load()).nvq_rope, "nvq_rope", dev, x.data_ptr(), _dtype_code(x), T, H, D, ld_t, ld_h,
+          positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel(), 1 if interleaved else 0,
+          magnitude, 1 if inverse else 0, out.data_ptr(), old_t, old_h)
     return out
 
 
@@ -629,14 +627,15 @@ class KvCache:
         _typed(k_scale, "k_scale", torch.float32, 1)
         _typed(v_scale, "v_scale", torch.float32, 1)
         self.device = k_codes.device
-        _same_device(self.device, k_scales=k_scales, v_codes=v_codes, v_scales=v_scales,
-                     k_scale=k_scale, v_scale=v_scale)
+        _on(self.device, k_scales=k_scales, v_codes=v_codes, v_scales=v_scales, k_scale=k_scale,
+            v_scale=v_scale)
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.k_scale, self.v_scale = k_scale, v_scale
         self.num_pages, self.heads, self.page_size, self.head_dim = P, H, S, D
         self.args = KvCacheArgs(ctypes.sizeof(KvCacheArgs), k_codes.data_ptr(), k_scales.data_ptr(),
                                 v_codes.data_ptr(), v_scales.data_ptr(), k_scale.data_ptr(),
                                 v_scale.data_ptr(), P, S, H, D)
+        self._ref = ctypes.byref(self.args)
 
     @classmethod
     def empty(cls, num_pages, heads, page_size, head_dim, k_amax, v_amax, device="cuda"):
@@ -656,17 +655,16 @@ def nvq_kv_append(cache, k, v, slots, ws=None):
     """Quantizes the new tokens k, v [T, heads, D] (bf16/fp32, tokens and heads
     may be strided) into the cache's slots [T] int32 (page * page_size + offset,
     negative: skipped).  ws (optional, >= 256 bytes) receives the status word."""
-    T, H, D, k_t, k_h = _heads(k, "k", _HEAD_TYPES)
-    Tv, Hv, Dv, v_t, v_h = _heads(v, "v", _HEAD_TYPES)
-    if (T, H, D) != (Tv, Hv, Dv) or k.dtype != v.dtype or (H, D) != (cache.heads, cache.head_dim):
+    T, H, D, k_t, k_h = _heads(k, "k")
+    _, _, _, v_t, v_h = _heads(v, "v")
+    if k.shape != v.shape or k.dtype != v.dtype or H != cache.heads or D != cache.head_dim:
         raise ValueError(f"k and v must be [T, {cache.heads}, {cache.head_dim}] of one dtype, got "
                          f"{k.dtype} {list(k.shape)} and {v.dtype} {list(v.shape)}")
     _typed(slots, "slots", torch.int32, T)
-    _same_device(cache.device, k=k, v=v, slots=slots, ws=ws)
-    with _Device(cache.device) as stream:
-        _check("nvq_kv_append", load().nvq_kv_append(
-            ctypes.byref(cache.args), k.data_ptr(), v.data_ptr(), _dtype_code(k), T, k_t, k_h, v_t, v_h,
-            slots.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(), stream))
+    _on(cache.device, k=k, v=v, slots=slots, ws=ws)
+    _call((_lib or load()).nvq_kv_append, "nvq_kv_append", cache.device, cache._ref, k.data_ptr(),
+          v.data_ptr(), _dtype_code(k), T, k_t, k_h, v_t, v_h, slots.data_ptr(),
+          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
 
 
 def nvq_kv_gather(cache, slots, out_dtype=torch.bfloat16, out=None, ws=None):
@@ -678,17 +676,15 @@ def nvq_kv_gather(cache, slots, out_dtype=torch.bfloat16, out=None, ws=None):
     if out is None:
         if out_dtype not in _HEAD_TYPES:
             raise ValueError(f"unsupported dtype {out_dtype}")
-        k = torch.empty(shape, dtype=out_dtype, device=cache.device)
-        v = torch.empty(shape, dtype=out_dtype, device=cache.device)
+        k, v = torch.empty((2, *shape), dtype=out_dtype, device=cache.device).unbind(0)
     else:
         k, v = out
         _typed(k, "k", k.dtype, *shape)
         _typed(v, "v", k.dtype, *shape)
-    _same_device(cache.device, slots=slots, k=k, v=v, ws=ws)
-    with _Device(cache.device) as stream:
-        _check("nvq_kv_gather", load().nvq_kv_gather(
-            ctypes.byref(cache.args), slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), _dtype_code(k),
-            _ptr(ws), 0 if ws is None else ws.numel(), stream))
+    _on(cache.device, slots=slots, k=k, v=v, ws=ws)
+    _call((_lib or load()).nvq_kv_gather, "nvq_kv_gather", cache.device, cache._ref, slots.data_ptr(), T,
+          k.data_ptr(), v.data_ptr(), _dtype_code(k), None if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel())
     return k, v
 
 
@@ -700,41 +696,46 @@ def nvq_paged_attention(q, cache, cu_q, kv_len, block_table, max_q=None, scale=N
     cu_q [B + 1], kv_len [B], block_table [B, width] int32 (rows may be
     strided).  max_q: no sequence has more new tokens (default: all of them).
     scale defaults to D^-1/2.  lse: optional fp32 [total_q, q_heads] to receive
-    the log-sum-exp.  Returns out, bf16 like q."""
+    the log-sum-exp.  ws: a workspace to reuse (default: one for the call).
+    Returns out, bf16 like q."""
     T, Hq, D, ld_t, ld_h = _heads(q, "q", (torch.bfloat16,))
+    dev = cache.device
     if D != cache.head_dim:
         raise ValueError(f"q must have the cache's head_dim {cache.head_dim}, got {D}")
     B = kv_len.numel()
     _typed(cu_q, "cu_q", torch.int32, B + 1)
     _typed(kv_len, "kv_len", torch.int32, B)
-    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype != torch.int32 or (
-            block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError(f"block_table must be int32 [{B}, width] with unit column stride")
-    width = block_table.shape[1]
-    table_ld = block_table.stride(0) if B > 1 else width
-    if B > 1 and table_ld < width:
-        raise ValueError("block_table rows must not overlap")
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be int32 [{B}, width]")
+    width = table_ld = block_table.shape[1]
+    if not block_table.is_contiguous():
+        table_ld, unit = block_table.stride()
+        if B == 1:
+            table_ld = width
+        if (width > 1 and unit != 1) or table_ld < width:
+            raise ValueError("block_table must have unit column stride and rows that do not overlap")
+    o_t = o_h = 0
     if out is None:
-        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
-        o_t = o_h = 0
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
     else:
         if out.shape != q.shape:
             raise ValueError("out must have the shape of q")
         _, _, _, o_t, o_h = _heads(out, "out", (torch.bfloat16,))
     if lse is not None:
         _typed(lse, "lse", torch.float32, T, Hq)
-    _same_device(cache.device, q=q, cu_q=cu_q, kv_len=kv_len, block_table=block_table, out=out, lse=lse,
-                 ws=ws)
+    _on(dev, q=q, cu_q=cu_q, kv_len=kv_len, block_table=block_table, out=out, lse=lse, ws=ws)
     a = PagedAttentionArgs(
-        ctypes.sizeof(PagedAttentionArgs), T, B, 0 if max_q is None else max_q, Hq, int(bool(causal)),
-        window, D ** -0.5 if scale is None else scale, q.data_ptr(), ld_t, ld_h, cu_q.data_ptr(),
+        _ATTENTION_SIZE, T, B, 0 if max_q is None else max_q, Hq, 1 if causal else 0, window,
+        D ** -0.5 if scale is None else scale, q.data_ptr(), ld_t, ld_h, cu_q.data_ptr(),
         kv_len.data_ptr(), block_table.data_ptr(), width, table_ld, out.data_ptr(), o_t, o_h,
         None if lse is None else lse.data_ptr(), None, 0)
-    L = load()
-    with _Device(cache.device) as stream:
-        if ws is None:
-            ws = workspace(L.nvq_paged_attention_workspace_bytes(ctypes.byref(cache.args), ctypes.byref(a)),
-                           cache.device)
-        a.ws, a.ws_bytes = ws.data_ptr(), ws.numel()
-        _check("nvq_paged_attention", L.nvq_paged_attention(ctypes.byref(cache.args), ctypes.byref(a), stream))
+    L = _lib or load()
+    ref = ctypes.byref(a)
+    if ws is None:
+        ws = torch.empty(L.nvq_paged_attention_workspace_bytes(cache._ref, ref), dtype=torch.uint8, device=dev)
+    a.ws, a.ws_bytes = ws.data_ptr(), ws.numel()
+    _call(L.nvq_paged_attention, "nvq_paged_attention", dev, cache._ref, ref)
     return out
+
+
+_ATTENTION_SIZE = ctypes.sizeof(PagedAttentionArgs)
