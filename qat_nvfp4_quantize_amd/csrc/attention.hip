@@ -151,6 +151,7 @@ int attn_sizes(const nvq_kv_cache* cache, const nvq_paged_attention_args* a, Att
       a->q_heads % cache->heads)
     return NVQ_ESHAPE;
   if (a->table_width > INT32_MAX / ps || a->B * cache->heads > (1 << 22) ||
+      a->B * (a->table_width * ps / 128 + 2) > INT32_MAX ||
       a->total_q * a->q_heads > (1 << 30))
     return NVQ_ESHAPE;
   p.total_q = (int)a->total_q, p.B = (int)a->B;
@@ -178,9 +179,9 @@ Plan attn_plan(const AttnParams& p, void* ws) {
   Plan plan{};
   WsCarve c(ws);
   if (p.c.D == 64 || p.c.D == 128 || p.c.D == 256) {
-    int tiles = attn_rows_tiles((int64_t)p.max_q * p.g);
+    int tiles = attn_rows_tiles(p.c.D, (int64_t)p.max_q * p.g);
     plan.use_chunk = tiles == 0;
-    if (plan.use_chunk && p.B > 1) tiles = attn_rows_tiles(p.g);  // single tokens beside the chunks
+    if (plan.use_chunk && p.B > 1) tiles = attn_rows_tiles(p.c.D, p.g);  // single tokens beside the chunks
     plan.use_rows = tiles > 0;
     if (plan.use_rows) attn_rows_plan(p, tiles, c, plan.rows);
     if (plan.use_chunk) attn_chunk_plan(p, 16 * tiles, !plan.use_rows, c, plan.chunk);

@@ -20,11 +20,14 @@
 // by 15 (in powers of two): weights stay within fp16, and a step without a
 // move rescales nothing.
 //
-// Work is split over the keys: the pieces of all sequences are sized from the
-// lengths on the device (every wave computes the same plan from cu_q and
-// kv_len), a workgroup per piece and key/value head, its four waves taking
-// 32 keys of each 128 in turn; pieces of a split sequence are joined by a
-// second kernel.
+// Work is split over the keys: per key/value head, the 128-key units of all
+// sequences in one row are dealt to as many workgroups as the chip holds at
+// once, in equal runs, whatever the lengths (every wave finds its run from
+// cu_q and kv_len itself; each of a workgroup's four waves takes 32 keys of a
+// unit).  A run may end inside a sequence: the parts of such sequences are
+// joined by a second kernel.  Equal runs matter: with pieces cut per sequence
+// 64 ragged sequences made 1232 pieces for 768 places, two rounds of 33 us
+// (83 us the call).
 
 #include <hip/hip_runtime.h>
 
@@ -35,6 +38,7 @@
 #include "nvq_dequant.h"
 #include "nvq_device.h"
 #include "nvq_internal.h"
+#include "nvq_scan.h"
 
 namespace nvq {
 namespace {
@@ -60,52 +64,22 @@ __device__ __forceinline__ Range key_range(const AttnParams& p, const Seq& s) {
   return r;
 }
 
-__device__ __forceinline__ int64_t wave_sum_i64(int64_t v) {
-#pragma unroll
-  for (int x = 1; x < 64; x <<= 1) v += __shfl_xor(v, x, 64);
-  return v;
+// Units up to and with sequence 64 c + lane, within its chunk of 64.
+__device__ __forceinline__ int chunk_units(const AttnParams& p, int max_rows, int c) {
+  const int b = 64 * c + (threadIdx.x & 63);
+  int units = 0;
+  if (b < p.B) {
+    const Seq s = load_seq(p, b);
+    if (s.n > 0 && s.n * p.g <= max_rows) units = key_range(p, s).units;
+  }
+  return wave_inclusive_scan(units);
 }
 
-struct Piece {
-  int b, index, count, units;
-};
+constexpr int kMinUnits = 2;  // units of a workgroup's run, where there are so many
 
-// Piece `item` of the plan (the same for every key/value head); false past
-// the last one.  All lanes return the same values.
-__device__ __forceinline__ bool find_piece(const AttnParams& p, const RowsPlan& plan, int item, Piece& out) {
-  const int lane = threadIdx.x & 63;
-  auto units_of = [&](int b) -> int {
-    if (b >= p.B) return 0;
-    const Seq s = load_seq(p, b);
-    return (s.n == 0 || s.n * p.g > plan.max_rows) ? 0 : key_range(p, s).units;
-  };
-  const int first = units_of(lane);
-  int64_t total = first;
-  for (int b0 = 64; b0 < p.B; b0 += 64) total += units_of(b0 + lane);
-  total = wave_sum_i64(total);
-  const int64_t per = max<int64_t>((total * p.c.H + plan.target - 1) / plan.target, plan.min_units);
-  int before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 64) {
-    const int units = b0 == 0 ? first : units_of(b0 + lane);
-    const int n = (int)((units + per - 1) / per);
-    int incl = n;
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) {
-      const int up = __shfl_up(incl, x, 64);
-      if (lane >= x) incl += up;
-    }
-    const uint64_t past = __ballot(before + incl > item);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      out.b = b0 + l;
-      out.count = __builtin_amdgcn_readlane(n, l);
-      out.index = item - (before + __builtin_amdgcn_readlane(incl, l) - out.count);
-      out.units = __builtin_amdgcn_readlane(units, l);
-      return true;
-    }
-    before += __builtin_amdgcn_readlane(incl, 63);
-  }
-  return false;
+// Workgroups of a kernel variant that a CU holds (its register budget).
+constexpr int rows_wgs_per_cu(int D, int MT) {
+  return D * MT <= 64 ? 4 : D * MT <= 128 ? 3 : D * MT <= 256 ? 2 : 1;
 }
 
 // Codes and scales of one wave step (32 keys) in registers.
@@ -192,38 +166,69 @@ __device__ __forceinline__ half2_t scale_two(uint32_t four, int i) {
 }
 
 template <int D, int MT>
-__global__ __launch_bounds__(256, D * MT > 256 ? 1 : 2) void k_attn_rows(AttnParams p, RowsPlan plan) {
+__global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnParams p, RowsPlan plan) {
   constexpr int kRows = 16 * MT, kTiles = D / 16, kSteps = D / 32;
   constexpr int kPitch = D + 4;  // floats; 16-byte rows shifted over the banks
   __shared__ float s_o[2][kRows * kPitch];
   __shared__ float s_m[4][kRows], s_l[4][kRows];
   __shared__ CheckLds s_check;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int n = lane & 15, q = lane >> 4;
-  if (blockIdx.x == 0) {  // one workgroup more than pieces
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (blockIdx.x == 0) {  // one workgroup more than workers
     check_batch(p, s_check);
     return;
   }
-  const int block = blockIdx.x - 1, kvh = block % p.c.H, item = block / p.c.H;
-  Piece pc;
-  if (!find_piece(p, plan, item, pc)) return;
-  const Seq s = load_seq(p, pc.b);
-  const Range range = key_range(p, s);
-  const int u_begin = (int)((int64_t)pc.index * pc.units / pc.count);
-  const int u_end = (int)((int64_t)(pc.index + 1) * pc.units / pc.count);
-  if (pc.index == 0 && kvh == 0 && threadIdx.x == 0) {
-    plan.seq[2 * pc.b] = item;
-    plan.seq[2 * pc.b + 1] = pc.count;
-  }
+  const int block = blockIdx.x - 1, kvh = block % p.c.H, worker = block / p.c.H;
+
+  // this worker's run [x, x_end) of the units of all sequences
+  int chunk = 0, incl = chunk_units(p, plan.max_rows, 0), total = __builtin_amdgcn_readlane(incl, 63);
+  for (int c = 1; 64 * c < p.B; ++c) total += __builtin_amdgcn_readlane(chunk_units(p, plan.max_rows, c), 63);
+  const int workers = min(plan.workers, max(1, total / kMinUnits));
+  if (worker >= workers || total == 0) return;
+  int x = (int)((int64_t)worker * total / workers);
+  const int x_begin = x, x_end = (int)((int64_t)(worker + 1) * total / workers);
+  int before = 0;  // units of earlier chunks
+  const float c0 = p.scale_log2 * *p.c.k_st, v_st = *p.c.v_st;
+
+#pragma unroll 1
+  while (x < x_end) {
+    // Made anew for each sequence: what the compiler would otherwise carry
+    // over from one to the next in registers ends in scratch memory, whose
+    // loads then wait in line with the cache's.
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int n = lane & 15, q = lane >> 4;
+    // the sequence of unit x, and the units of it in this run
+    uint64_t past = __ballot(before + incl > x);
+    while (!past) {
+      if (64 * (chunk + 1) >= p.B) return;  // only if the arrays change under the call
+      before += __builtin_amdgcn_readlane(incl, 63);
+      incl = chunk_units(p, plan.max_rows, ++chunk);
+      past = __ballot(before + incl > x);
+    }
+    const int sl = __builtin_ctzll(past), b = 64 * chunk + sl;
+    const Seq s = load_seq(p, b);
+    const Range range = key_range(p, s);
+    const int seq_x = before + __builtin_amdgcn_readlane(incl, sl) - range.units;  // its first unit
+    const int u_begin = x - seq_x, u_end = min(range.units, x_end - seq_x);
+    // a part that starts a run goes to the worker's slot 0, one that ends it
+    // inside a sequence begun within the run to slot 1
+    const bool whole_seq = u_begin == 0 && u_end == range.units;
+    const int slot = x == x_begin ? 2 * worker : 2 * worker + 1;
+    if (u_begin == 0 && kvh == 0 && threadIdx.x == 0) {
+      const int last = (int)(((int64_t)(seq_x + range.units) * workers - 1) / total);
+      plan.seq[2 * b] = slot;
+      plan.seq[2 * b + 1] = last - worker + 1;
+    }
+    if (x != x_begin) __syncthreads();  // the last sequence's LDS reads are done
+    x = seq_x + u_end;
   const int rows = s.n * p.g;
-  const int32_t* table = p.table + pc.b * p.table_ld;
+  const int32_t* table = p.table + b * p.table_ld;
 
   // Q in fp16 under a power of two per row that brings its largest magnitude
   // to 2^14 .. 2^15: bf16's 8 bits are kept down to 2^-38 of it.
   half8_t qf[MT][kSteps];
   float cq[MT];
   int see_lo[MT], see_hi[MT];
-  const float c0 = p.scale_log2 * *p.c.k_st;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     const int r = 16 * mt + n, i = r / p.g, h = kvh * p.g + (r - i * p.g);
@@ -367,19 +372,17 @@ __global__ __launch_bounds__(256, D * MT > 256 ? 1 : 2) void k_attn_rows(AttnPar
       }
     }
   };
-  // two register sets in turn: the next step's loads are in flight while a
-  // step is computed, and nothing is copied
-  StepRegs<D> even, odd;
-  int id_even[2], id_odd[2];
+  // the next step's loads are in flight while a step is computed
+  StepRegs<D> cur, nxt;
+  int id_cur[2], id_nxt[2];
   fetch_ids(u_begin);
-  fetch(even, id_even, u_begin);
+  fetch(cur, id_cur, u_begin);
 #pragma unroll 1
-  for (int u = u_begin; u < u_end; u += 2) {
-    if (u + 1 < u_end) fetch(odd, id_odd, u + 1);
-    consume(even, id_even, u);
-    if (u + 1 >= u_end) break;
-    if (u + 2 < u_end) fetch(even, id_even, u + 2);
-    consume(odd, id_odd, u + 1);
+  for (int u = u_begin; u < u_end; ++u) {
+    if (u + 1 < u_end) fetch(nxt, id_nxt, u + 1);
+    consume(cur, id_cur, u);
+    cur = nxt;
+    id_cur[0] = id_nxt[0], id_cur[1] = id_nxt[1];
   }
 
   // Join the four waves: each scales its part to the common reference, waves
@@ -419,7 +422,6 @@ __global__ __launch_bounds__(256, D * MT > 256 ? 1 : 2) void k_attn_rows(AttnPar
       *at = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
     });
   __syncthreads();
-  const float v_st = *p.c.v_st;
   constexpr int kChunks = D / 8;
   for (int e = threadIdx.x; e < kRows * kChunks; e += 256) {
     const int r = e / kChunks, ch = e - r * kChunks;
@@ -436,7 +438,7 @@ __global__ __launch_bounds__(256, D * MT > 256 ? 1 : 2) void k_attn_rows(AttnPar
       const float4 b = *reinterpret_cast<const float4*>(s_o[1] + r * kPitch + 8 * ch + 4 * i);
       x[4 * i] = a.x + b.x, x[4 * i + 1] = a.y + b.y, x[4 * i + 2] = a.z + b.z, x[4 * i + 3] = a.w + b.w;
     }
-    if (pc.count == 1) {
+    if (whole_seq) {
       const int i = r / p.g, h = kvh * p.g + (r - i * p.g);
       const float inv = sum == 0.0f ? 0.0f : v_st / sum;
       uint32_t w[4];
@@ -448,17 +450,18 @@ __global__ __launch_bounds__(256, D * MT > 256 ? 1 : 2) void k_attn_rows(AttnPar
       if (p.lse && ch == 0)
         p.lse[(int64_t)(s.row0 + i) * p.Hq + h] = sum == 0.0f ? -INFINITY : (m + __builtin_log2f(sum)) * kLn2;
     } else {
-      const int64_t slot = (int64_t)block * kRows + r;
-      float4* at = reinterpret_cast<float4*>(plan.part_o + slot * D + 8 * ch);
+      const int64_t at_row = ((int64_t)slot * p.c.H + kvh) * kRows + r;
+      float4* at = reinterpret_cast<float4*>(plan.part_o + at_row * D + 8 * ch);
       at[0] = make_float4(x[0], x[1], x[2], x[3]);
       at[1] = make_float4(x[4], x[5], x[6], x[7]);
-      if (ch == 0) plan.part_ml[slot] = make_float2(m, sum);
+      if (ch == 0) plan.part_ml[at_row] = make_float2(m, sum);
     }
+  }
   }
 }
 
-// Joins the pieces of a split sequence: a workgroup per row and key/value
-// head, its four waves taking pieces in turn, a lane D / 64 elements.
+// Joins the parts of a split sequence: a workgroup per row and key/value
+// head, its four waves taking parts in turn, a lane D / 64 elements.
 template <int D, int kRows>
 __global__ __launch_bounds__(256) void k_attn_rows_join(AttnParams p, RowsPlan plan) {
   constexpr int kE = D / 64;
@@ -467,10 +470,13 @@ __global__ __launch_bounds__(256) void k_attn_rows_join(AttnParams p, RowsPlan p
   const int b = blockIdx.x, kvh = blockIdx.y, r = blockIdx.z;
   const Seq s = load_seq(p, b);
   if (r >= s.n * p.g || s.n * p.g > plan.max_rows) return;
-  const int item = plan.seq[2 * b], count = plan.seq[2 * b + 1];
+  const int first = plan.seq[2 * b], count = plan.seq[2 * b + 1];
   if (count == 1) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  auto slot = [&](int i) { return ((int64_t)(item + i) * p.c.H + kvh) * kRows + r; };
+  // the first worker's slot as noted, slot 0 of the others
+  auto slot = [&](int i) {
+    return ((int64_t)(i == 0 ? first : 2 * ((first >> 1) + i)) * p.c.H + kvh) * kRows + r;
+  };
   float m = -INFINITY;
   for (int i = threadIdx.x; i < count; i += 256) m = fmaxf(m, plan.part_ml[slot(i)].x);
 #pragma unroll
@@ -507,7 +513,7 @@ __global__ __launch_bounds__(256) void k_attn_rows_join(AttnParams p, RowsPlan p
 
 template <int D, int MT>
 int launch_rows(const AttnParams& p, const RowsPlan& plan, hipStream_t s) {
-  hipLaunchKernelGGL((k_attn_rows<D, MT>), dim3((unsigned)(plan.items * p.c.H + 1)), dim3(256), 0, s, p, plan);
+  hipLaunchKernelGGL((k_attn_rows<D, MT>), dim3((unsigned)(plan.workers * p.c.H + 1)), dim3(256), 0, s, p, plan);
   if (int rc = last_launch()) return rc;
   if (!plan.may_split) return NVQ_OK;
   const int rows = std::min<int64_t>((int64_t)p.max_q * p.g, 16 * MT);
@@ -520,31 +526,33 @@ int launch_rows(const AttnParams& p, const RowsPlan& plan, hipStream_t s) {
 
 // Row tiles of 16 that the kernel takes for sequences of up to `rows` rows per
 // key/value head; 0: none.
-int attn_rows_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 0; }
+int attn_rows_tiles(int D, int64_t rows) {
+  return rows <= (D == 256 ? 32 : 64) ? (int)((rows + 15) / 16) : 0;
+}
 
 void attn_rows_plan(const AttnParams& p, int tiles, WsCarve& ws, RowsPlan& plan) {
   plan.max_rows = 16 * tiles;
-  plan.min_units = kRowsMinUnits;
-  plan.target = kRowsTarget;
-  const int64_t units = (p.num_keys + 31 + kUnit - 1) / kUnit;  // most of a sequence
-  plan.may_split = units > plan.min_units;
-  // pieces: ceil(units / per) each, per >= total H / target and >= min_units
-  const int64_t by_target = (plan.target + p.c.H - 1) / p.c.H + p.B;
-  const int64_t by_units = p.B * std::max<int64_t>(1, (units + plan.min_units - 1) / plan.min_units);
-  plan.items = std::min(by_target, by_units);
+  const int64_t units = (p.num_keys + kUnit - 1) / kUnit + 1;  // most of a sequence
+  const int64_t places = (int64_t)rows_wgs_per_cu(p.c.D, tiles) * device_cu_count();
+  plan.workers = (int)std::max<int64_t>(1, std::min((places - 1) / p.c.H, units * p.B / kMinUnits));
+  plan.may_split = plan.workers > 1;
   plan.seq = ws.take<int32_t>(2 * (size_t)p.B);
-  const size_t slots = plan.may_split ? (size_t)(plan.items * p.c.H) * plan.max_rows : 0;
-  plan.part_ml = ws.take<float2>(slots);
-  plan.part_o = ws.take<float>(slots * p.c.D);
+  const size_t rows = plan.may_split ? (size_t)(2 * plan.workers * p.c.H) * plan.max_rows : 0;
+  plan.part_ml = ws.take<float2>(rows);
+  plan.part_o = ws.take<float>(rows * p.c.D);
 }
 
 int attn_rows_launch(const AttnParams& p, const RowsPlan& plan, hipStream_t s) {
-  switch (p.c.D * 4 + plan.max_rows / 16) {
-    case 64 * 4 + 1: return launch_rows<64, 1>(p, plan, s);
-    case 64 * 4 + 2: return launch_rows<64, 2>(p, plan, s);
-    case 128 * 4 + 1: return launch_rows<128, 1>(p, plan, s);
-    case 128 * 4 + 2: return launch_rows<128, 2>(p, plan, s);
-    case 256 * 4 + 1: return launch_rows<256, 1>(p, plan, s);
+  switch (p.c.D * 8 + plan.max_rows / 16) {
+    case 64 * 8 + 1: return launch_rows<64, 1>(p, plan, s);
+    case 64 * 8 + 2: return launch_rows<64, 2>(p, plan, s);
+    case 64 * 8 + 3: return launch_rows<64, 3>(p, plan, s);
+    case 64 * 8 + 4: return launch_rows<64, 4>(p, plan, s);
+    case 128 * 8 + 1: return launch_rows<128, 1>(p, plan, s);
+    case 128 * 8 + 2: return launch_rows<128, 2>(p, plan, s);
+    case 128 * 8 + 3: return launch_rows<128, 3>(p, plan, s);
+    case 128 * 8 + 4: return launch_rows<128, 4>(p, plan, s);
+    case 256 * 8 + 1: return launch_rows<256, 1>(p, plan, s);
     default: return launch_rows<256, 2>(p, plan, s);
   }
 }

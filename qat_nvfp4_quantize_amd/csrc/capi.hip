@@ -3,6 +3,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <atomic>
+
 #include "nvq.h"
 #include "nvq_internal.h"
 
@@ -13,11 +15,17 @@ __global__ void k_status_clear(uint32_t* status) { *status = 0u; }
 }  // namespace
 
 int device_cu_count() {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> cached[kMaxDevices];
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return 256;
+  const bool keep = dev >= 0 && dev < kMaxDevices;
+  if (keep)
+    if (const int n = cached[dev].load(std::memory_order_relaxed)) return n;
   int n = 0;
   if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
     return 256;
+  if (keep) cached[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

@@ -26,21 +26,17 @@ struct AttnParams {
   uint32_t* status;
 };
 
-// Plan of the few-rows kernel, and where the pieces of split sequences go.
+// Plan of the few-rows kernel, and where the parts of split sequences go.
 struct RowsPlan {
-  int max_rows;   // sequences with more rows per key/value head are left out
-  int min_units;  // smallest piece, in 128-key units
-  int target;     // pieces times heads aimed at
+  int max_rows;  // sequences with more rows per key/value head are left out
+  int workers;   // most workgroups per key/value head
   int may_split;
-  int64_t items;     // most pieces there can be
-  int32_t* seq;      // [B][2] first piece and their number
-  float2* part_ml;   // [piece][head][max_rows] reference and sum
-  float* part_o;     // [piece][head][max_rows][D]
+  int32_t* seq;     // [B][2]: first worker and its slot (2 worker + slot), number of workers
+  float2* part_ml;  // [worker][2 slots][head][max_rows] reference and sum
+  float* part_o;    // [worker][2 slots][head][max_rows][D]
 };
-constexpr int kRowsMinUnits = 2;
-constexpr int kRowsTarget = 1024;
 
-int attn_rows_tiles(int64_t rows);
+int attn_rows_tiles(int D, int64_t rows);
 void attn_rows_plan(const AttnParams& p, int tiles, WsCarve& ws, RowsPlan& plan);
 int attn_rows_launch(const AttnParams& p, const RowsPlan& plan, hipStream_t s);
 

@@ -6,6 +6,19 @@
 
 namespace nvq {
 
+// Inclusive prefix sum of v over the 64 lanes of a wave (all active), in DPP
+// steps: shifts by 1, 2, 4 and 8 within each row of 16 lanes, then the row
+// totals handed to the next rows.  No LDS permutes.
+__device__ __forceinline__ int wave_inclusive_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);  // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);  // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);  // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+  return v;
+}
+
 // Inclusive prefix sum of v over the workgroup, in thread order.  blockDim.x
 // is a multiple of 64 and at most 1024; every thread of the workgroup calls
 // it; s_wave holds 16 ints of LDS.  Lane scans with __shfl_up, then wave 0
