@@ -148,15 +148,15 @@ struct TileRegs {
   uint32_t k[D / 32], v[D / 32], ks, vs;
 };
 
-template <int kN>
-__device__ __forceinline__ void load_codes(uint32_t (&w)[kN], const uint8_t* at) {
-  if constexpr (kN == 2) {
-    const uint2 x = *reinterpret_cast<const uint2*>(at);
+template <int D>
+__device__ __forceinline__ void load_codes(uint32_t (&w)[D / 32], const uint8_t* row, int part) {
+  if constexpr (D == 64) {
+    const uint2 x = *reinterpret_cast<const uint2*>(row + 8 * part);
     w[0] = x.x, w[1] = x.y;
   } else {
 #pragma unroll
-    for (int i = 0; i < kN / 4; ++i) {
-      const uint4 x = reinterpret_cast<const uint4*>(at)[i];
+    for (int i = 0; i < D / 128; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4*>(row + 64 * i + 16 * part);
       w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
     }
   }
@@ -165,47 +165,65 @@ __device__ __forceinline__ void load_codes(uint32_t (&w)[kN], const uint8_t* at)
 template <int D>
 __device__ __forceinline__ void load_tile(const AttnParams& p, TileRegs<D>& r, int id, int kvh, int off, int part) {
   const int64_t tile = ((int64_t)max(id, 0) * p.c.H + kvh) << p.c.log_ps;  // a masked key reads page 0
-  load_codes(r.k, p.c.k_codes + (tile + off) * (D / 2) + part * (D / 8));
-  load_codes(r.v, p.c.v_codes + (tile + off) * (D / 2) + part * (D / 8));
-  const uint8_t* ks = p.c.k_scales + (tile + off) * (D / 16) + part * (D / 64);
-  const uint8_t* vs = p.c.v_scales + tile * (D / 16) + ((int64_t)(part * (D / 64)) << p.c.log_ps) + off;
-  if constexpr (D == 64)
-    r.ks = *ks;
-  else if constexpr (D == 128)
-    r.ks = *reinterpret_cast<const uint16_t*>(ks);
-  else
-    r.ks = *reinterpret_cast<const uint32_t*>(ks);
-  r.vs = vs[0];
-  if constexpr (D >= 128) r.vs |= (uint32_t)vs[p.c.ps] << 8;
-  if constexpr (D >= 256) r.vs |= (uint32_t)vs[2 * p.c.ps] << 16 | (uint32_t)vs[3 * p.c.ps] << 24;
+  load_codes<D>(r.k, p.c.k_codes + (tile + off) * (D / 2), part);
+  load_codes<D>(r.v, p.c.v_codes + (tile + off) * (D / 2), part);
+  const uint8_t* ks = p.c.k_scales + (tile + off) * (D / 16);
+  const uint8_t* vs = p.c.v_scales + tile * (D / 16) + off;
+  const int64_t ps = p.c.ps;
+  if constexpr (D == 64) {
+    r.ks = ks[part];
+    r.vs = vs[part * ps];
+  } else {
+    r.ks = *reinterpret_cast<const uint16_t*>(ks + 2 * part);
+    r.vs = vs[2 * part * ps] | (uint32_t)vs[(2 * part + 1) * ps] << 8;
+    if constexpr (D == 256) {
+      r.ks |= (uint32_t)*reinterpret_cast<const uint16_t*>(ks + 8 + 2 * part) << 16;
+      r.vs |= (uint32_t)vs[(8 + 2 * part) * ps] << 16 | (uint32_t)vs[(9 + 2 * part) * ps] << 24;
+    }
+  }
 }
 
 // Dequantizes and writes to the LDS tiles; a key without a page becomes zeros.
 template <int D>
-__device__ __forceinline__ void store_tile(const TileRegs<D>& r, bool live, uint8_t* k, uint8_t* v) {
+__device__ __forceinline__ void store_tile(const TileRegs<D>& r, bool live, uint8_t* k, uint8_t* v, int part) {
   const uint32_t ks = live ? r.ks & 0x7F7F7F7Fu : 0u, vs = live ? r.vs & 0x7F7F7F7Fu : 0u;
 #pragma unroll
   for (int j = 0; j < D / 32; ++j) {
-    reinterpret_cast<half8_t*>(k)[j] = dequant8(r.k[j], scale_pair(ks, j >> 1));
-    reinterpret_cast<half8_t*>(v)[j] = dequant8(r.v[j], scale_pair(vs, j >> 1));
+    const int at = D == 64 ? 32 * part + 16 * j : 256 * (j >> 2) + 64 * part + 16 * (j & 3);
+    *reinterpret_cast<half8_t*>(k + at) = dequant8(r.k[j], scale_pair(ks, j >> 1));
+    *reinterpret_cast<half8_t*>(v + at) = dequant8(r.v[j], scale_pair(vs, j >> 1));
   }
 }
 
+// A tile in LDS: key k at (k % 4) kPlane + (k / 4) kRow.  Rows are 16 bytes past
+// a multiple of 256 (128 for D = 64) and planes 64, so that each access of 256
+// bytes a clock meets every bank once: the 16 keys of a 16-byte read, the 4
+// keys x 64 bytes of a transpose read, and the loader's writes (whose 16 lanes
+// take keys 4 apart).  A plain pitch of 2 D + 32 cost a quarter of the time in
+// bank conflicts.
 template <int D>
 struct ChunkLds {
-  // rows 32 bytes past a multiple of 256 (or 128): the 8 rows of a 16-byte
-  // read, and the 4 rows x 32 bytes of a transpose read, lie in other banks
-  static constexpr int kPitch = 2 * D + 32, kTile = kTileKeys * kPitch;
+  static constexpr int kRow = 2 * D + 16, kPlane = kTileKeys / 4 * kRow + 64;
+  static constexpr int kTile = 3 * kPlane + kTileKeys / 4 * kRow;
   alignas(16) uint8_t k[2][kTile];
   alignas(16) uint8_t v[2][kTile];
   alignas(16) uint32_t dead[2][4];  // any key of the wave's 16 without a page
   uint8_t live[2][kTileKeys];
+  static __device__ __forceinline__ int at(int key) { return (key & 3) * kPlane + (key >> 2) * kRow; }
 };
+
+// Largest of three (v_max3_f32; fmaxf would first quiet each operand).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float m;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(a), "v"(b), "v"(c));
+  return m;
+}
 
 template <int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams p, ChunkPlan plan) {
-  constexpr int kPitch = ChunkLds<D>::kPitch, kSteps = D / 16, kOut = D / 32;
-  __shared__ ChunkLds<D> lds;
+  using Lds = ChunkLds<D>;
+  constexpr int kSteps = D / 16, kOut = D / 32;
+  __shared__ Lds lds;
   if (plan.check && blockIdx.x == 0) {
     check_batch(p, reinterpret_cast<CheckLds&>(lds));
     return;
@@ -269,8 +287,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams
   for (int i = 0; i < kOut; ++i) o[i] = (floatx16_t)(0.0f);
   float ref = -INFINITY, ref_safe = 0.0f, l = 0.0f;
 
-  // loader: thread takes a quarter of key threadIdx.x / 4
-  const int lkey = threadIdx.x >> 2, part = threadIdx.x & 3;
+  // loader: thread takes a quarter of one key, 16 lanes keys 4 apart
+  const int part = threadIdx.x & 3, lkey = 16 * wave + 4 * ((lane >> 2) & 3) + (lane >> 4);
   auto page_of = [&](int u) {
     const int64_t key = range.base + (int64_t)u * kTileKeys + lkey;
     if (u >= u_end || key >= range.hi) return -1;
@@ -279,7 +297,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams
   };
   auto off_of = [&](int u) { return (int)(range.base + (int64_t)u * kTileKeys + lkey) & (p.c.ps - 1); };
   auto put = [&](const TileRegs<D>& t, int id, int buf) {
-    store_tile<D>(t, id >= 0, lds.k[buf] + lkey * kPitch + part * (D / 2), lds.v[buf] + lkey * kPitch + part * (D / 2));
+    store_tile<D>(t, id >= 0, lds.k[buf] + Lds::at(lkey), lds.v[buf] + Lds::at(lkey), part);
     if (part == 0) lds.live[buf][lkey] = id >= 0;
     const bool dead = __ballot(id < 0) != 0;
     if (lane == 0) lds.dead[buf][wave] = dead;
@@ -291,9 +309,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams
   put(regs, id, 0);
   __syncthreads();
 
-  // lane's source address of a transpose read: key row 4 h + s / 4, elements
+  // lane's source address of a transpose read: key 4 h + s / 4, elements
   // 16 (lane / 16 % 2) + 4 (s % 4), s = lane % 16
-  const int tr_off = (4 * h + ((lane & 15) >> 2)) * kPitch + 2 * (16 * ((lane >> 4) & 1) + 4 * (lane & 3));
+  const int tr_off = Lds::at(4 * h + ((lane & 15) >> 2)) + 2 * (16 * ((lane >> 4) & 1) + 4 * (lane & 3));
 #pragma unroll 1
   for (int u = u_begin; u < u_end; ++u) {
     const int buf = (u - u_begin) & 1;
@@ -308,7 +326,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
       sc[kt] = (floatx16_t)(0.0f);
-      const uint8_t* at = lds.k[buf] + (32 * kt + l32) * kPitch + 16 * h;
+      const uint8_t* at = lds.k[buf] + Lds::at(32 * kt + l32) + 16 * h;
 #pragma unroll
       for (int w = 0; w < kSteps; ++w)
         sc[kt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const half8_t*>(at + 32 * w), qf[w], sc[kt],
@@ -324,9 +342,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams
           sc[kt][v] = (key >= see_lo && key < see_hi && lds.live[buf][k]) ? sc[kt][v] : -INFINITY;
         }
     }
-    float top = fmaxf(sc[0][0], sc[1][0]);
+    float top = max3(sc[0][0], sc[1][0], sc[1][1]), top2 = max3(sc[0][1], sc[0][2], sc[1][2]);
 #pragma unroll
-    for (int v = 1; v < 16; ++v) top = fmaxf(top, fmaxf(sc[0][v], sc[1][v]));
+    for (int v = 3; v < 15; v += 2) {
+      top = max3(top, sc[0][v], sc[1][v]);
+      top2 = max3(top2, sc[0][v + 1], sc[1][v + 1]);
+    }
+    top = max3(top, sc[0][15], sc[1][15]);
+    top = fmaxf(top, top2);
     top *= cq;
     if (__ballot(top > ref + kRefRoom)) {
       top = fmaxf(top, __shfl_xor(top, 32, 64));
@@ -352,7 +375,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams
     for (int i = 0; i < kOut; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(tr_pair(vt + 16 * j * kPitch + 64 * i, 8 * kPitch), pf[j], o[i],
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(tr_pair(vt + 4 * j * Lds::kRow + 64 * i, 2 * Lds::kRow), pf[j], o[i],
                                                       0, 0, 0);
     if (more) put(regs, id, buf ^ 1);
     __syncthreads();
