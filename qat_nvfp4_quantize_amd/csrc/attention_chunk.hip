@@ -145,53 +145,61 @@ __device__ __forceinline__ half8_t tr_pair(const NVQ_LDS char* at, int second) {
 // Codes and scales of a quarter of one key's elements, K and V.
 template <int D>
 struct TileRegs {
-  uint32_t k[D / 32], v[D / 32], ks, vs;
+  uint32_t k[D / 32], v[D / 32], ks[D / 128], vs[D / 64];
+};
+template <>
+struct TileRegs<64> {
+  uint32_t k[2], v[2], ks, vs;
 };
 
+// A wave loads 16 keys of a tile, which lie in one page: its base is uniform,
+// and a lane's offsets in it (key16 of the 16 keys, quarter `part` of the
+// elements) never change.  id < 0 (no such page) reads page 0, masked later.
 template <int D>
-__device__ __forceinline__ void load_codes(uint32_t (&w)[D / 32], const uint8_t* row, int part) {
+__device__ __forceinline__ void load_tile(const AttnParams& p, TileRegs<D>& r, int id, int kvh, int off,
+                                          uint32_t key16, uint32_t part) {
+  const int64_t tile = ((int64_t)max(id, 0) * p.c.H + kvh) << p.c.log_ps;
+  const uint8_t* kc = p.c.k_codes + (tile + off) * (D / 2);
+  const uint8_t* vc = p.c.v_codes + (tile + off) * (D / 2);
+  const uint8_t* ks = p.c.k_scales + (tile + off) * (D / 16);
+  const uint8_t* vs = p.c.v_scales + tile * (D / 16) + off;
+  const uint32_t at = key16 * (D / 2), sat = key16 * (D / 16);
   if constexpr (D == 64) {
-    const uint2 x = *reinterpret_cast<const uint2*>(row + 8 * part);
-    w[0] = x.x, w[1] = x.y;
+    const uint2 x = *reinterpret_cast<const uint2*>(kc + (at + 8 * part));
+    const uint2 y = *reinterpret_cast<const uint2*>(vc + (at + 8 * part));
+    r.k[0] = x.x, r.k[1] = x.y, r.v[0] = y.x, r.v[1] = y.y;
+    r.ks = ks[sat + part];
+    r.vs = vs[key16 + (part << p.c.log_ps)];
   } else {
 #pragma unroll
     for (int i = 0; i < D / 128; ++i) {
-      const uint4 x = *reinterpret_cast<const uint4*>(row + 64 * i + 16 * part);
-      w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+      const uint4 x = *reinterpret_cast<const uint4*>(kc + (at + 16 * part) + 64 * i);
+      const uint4 y = *reinterpret_cast<const uint4*>(vc + (at + 16 * part) + 64 * i);
+      r.k[4 * i] = x.x, r.k[4 * i + 1] = x.y, r.k[4 * i + 2] = x.z, r.k[4 * i + 3] = x.w;
+      r.v[4 * i] = y.x, r.v[4 * i + 1] = y.y, r.v[4 * i + 2] = y.z, r.v[4 * i + 3] = y.w;
+      r.ks[i] = *reinterpret_cast<const uint16_t*>(ks + (sat + 2 * part) + 8 * i);
+      r.vs[2 * i] = vs[key16 + ((8 * i + 2 * part) << p.c.log_ps)];
+      r.vs[2 * i + 1] = vs[key16 + ((8 * i + 2 * part + 1) << p.c.log_ps)];
     }
   }
 }
 
-template <int D>
-__device__ __forceinline__ void load_tile(const AttnParams& p, TileRegs<D>& r, int id, int kvh, int off, int part) {
-  const int64_t tile = ((int64_t)max(id, 0) * p.c.H + kvh) << p.c.log_ps;  // a masked key reads page 0
-  load_codes<D>(r.k, p.c.k_codes + (tile + off) * (D / 2), part);
-  load_codes<D>(r.v, p.c.v_codes + (tile + off) * (D / 2), part);
-  const uint8_t* ks = p.c.k_scales + (tile + off) * (D / 16);
-  const uint8_t* vs = p.c.v_scales + tile * (D / 16) + off;
-  const int64_t ps = p.c.ps;
-  if constexpr (D == 64) {
-    r.ks = ks[part];
-    r.vs = vs[part * ps];
-  } else {
-    r.ks = *reinterpret_cast<const uint16_t*>(ks + 2 * part);
-    r.vs = vs[2 * part * ps] | (uint32_t)vs[(2 * part + 1) * ps] << 8;
-    if constexpr (D == 256) {
-      r.ks |= (uint32_t)*reinterpret_cast<const uint16_t*>(ks + 8 + 2 * part) << 16;
-      r.vs |= (uint32_t)vs[(8 + 2 * part) * ps] << 16 | (uint32_t)vs[(9 + 2 * part) * ps] << 24;
-    }
-  }
-}
+// Byte of an E4M3 scale -> fp16 pair s_b * 2^-8, finite for any byte.
+__device__ __forceinline__ uint32_t scale_of(uint32_t byte) { return (byte & 0x7Fu) * 0x00800080u; }
 
-// Dequantizes and writes to the LDS tiles; a key without a page becomes zeros.
+// Dequantizes and writes to the LDS tiles.
 template <int D>
-__device__ __forceinline__ void store_tile(const TileRegs<D>& r, bool live, uint8_t* k, uint8_t* v, int part) {
-  const uint32_t ks = live ? r.ks & 0x7F7F7F7Fu : 0u, vs = live ? r.vs & 0x7F7F7F7Fu : 0u;
+__device__ __forceinline__ void store_tile(const TileRegs<D>& r, uint8_t* k, uint8_t* v, int part) {
 #pragma unroll
   for (int j = 0; j < D / 32; ++j) {
     const int at = D == 64 ? 32 * part + 16 * j : 256 * (j >> 2) + 64 * part + 16 * (j & 3);
-    *reinterpret_cast<half8_t*>(k + at) = dequant8(r.k[j], scale_pair(ks, j >> 1));
-    *reinterpret_cast<half8_t*>(v + at) = dequant8(r.v[j], scale_pair(vs, j >> 1));
+    uint32_t ks, vs;
+    if constexpr (D == 64)
+      ks = scale_of(r.ks), vs = scale_of(r.vs);
+    else
+      ks = scale_of((j >> 1) & 1 ? r.ks[j >> 2] >> 8 : r.ks[j >> 2]), vs = scale_of(r.vs[j >> 1]);
+    *reinterpret_cast<half8_t*>(k + at) = dequant8(r.k[j], ks);
+    *reinterpret_cast<half8_t*>(v + at) = dequant8(r.v[j], vs);
   }
 }
 
@@ -207,8 +215,7 @@ struct ChunkLds {
   static constexpr int kTile = 3 * kPlane + kTileKeys / 4 * kRow;
   alignas(16) uint8_t k[2][kTile];
   alignas(16) uint8_t v[2][kTile];
-  alignas(16) uint32_t dead[2][4];  // any key of the wave's 16 without a page
-  uint8_t live[2][kTileKeys];
+  alignas(16) uint32_t dead[2][4];  // 16 keys without a page
   static __device__ __forceinline__ int at(int key) { return (key & 3) * kPlane + (key >> 2) * kRow; }
 };
 
@@ -287,26 +294,33 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams
   for (int i = 0; i < kOut; ++i) o[i] = (floatx16_t)(0.0f);
   float ref = -INFINITY, ref_safe = 0.0f, l = 0.0f;
 
-  // loader: thread takes a quarter of one key, 16 lanes keys 4 apart
-  const int part = threadIdx.x & 3, lkey = 16 * wave + 4 * ((lane >> 2) & 3) + (lane >> 4);
-  auto page_of = [&](int u) {
-    const int64_t key = range.base + (int64_t)u * kTileKeys + lkey;
-    if (u >= u_end || key >= range.hi) return -1;
-    const int id = table[key >> p.c.log_ps];
-    return id < p.c.num_pages ? id : -1;
-  };
-  auto off_of = [&](int u) { return (int)(range.base + (int64_t)u * kTileKeys + lkey) & (p.c.ps - 1); };
-  auto put = [&](const TileRegs<D>& t, int id, int buf) {
-    store_tile<D>(t, id >= 0, lds.k[buf] + Lds::at(lkey), lds.v[buf] + Lds::at(lkey), part);
-    if (part == 0) lds.live[buf][lkey] = id >= 0;
-    const bool dead = __ballot(id < 0) != 0;
-    if (lane == 0) lds.dead[buf][wave] = dead;
+  // Loader: a wave takes 16 keys of the tile, a thread a quarter of one of
+  // them, 16 lanes keys 4 apart.  Page ids of the wave's next 64 tiles with one
+  // load (-1: no key, or an id outside the cache).
+  const int part = threadIdx.x & 3, key16 = 4 * ((lane >> 2) & 3) + (lane >> 4);
+  const int lkey_at = Lds::at(16 * wave + key16);
+  const int64_t base = range.base + 16 * wave;
+  int ids = -1, ids_at = u_begin;
+  auto fetch_ids = [&](int u0) {
+    const int64_t key = base + (int64_t)(u0 + lane) * kTileKeys;
+    const int id = (u0 + lane < u_end && key < range.hi) ? table[key >> p.c.log_ps] : -1;
+    ids = id < p.c.num_pages ? id : -1;
+    ids_at = u0;
   };
   TileRegs<D> regs;
-  int id = page_of(u_begin);
-  load_tile<D>(p, regs, id, kvh, off_of(u_begin), part);
-  int id_next = page_of(u_begin + 1);
-  put(regs, id, 0);
+  int id;
+  auto fetch = [&](int u) {  // past the last tile: page 0, never looked at
+    if (u - ids_at >= 64) fetch_ids(u);
+    id = __builtin_amdgcn_readlane(ids, u - ids_at);
+    load_tile<D>(p, regs, id, kvh, (int)(base + (int64_t)u * kTileKeys) & (p.c.ps - 1), key16, part);
+  };
+  auto put = [&](int buf) {
+    store_tile<D>(regs, lds.k[buf] + lkey_at, lds.v[buf] + lkey_at, part);
+    if (lane == 0) lds.dead[buf][wave] = id < 0;
+  };
+  fetch_ids(u_begin);
+  fetch(u_begin);
+  put(0);
   __syncthreads();
 
   // lane's source address of a transpose read: key 4 h + s / 4, elements
@@ -316,22 +330,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams
   for (int u = u_begin; u < u_end; ++u) {
     const int buf = (u - u_begin) & 1;
     const int64_t kb = range.base + (int64_t)u * kTileKeys;
-    const bool more = u + 1 < u_end;
-    if (more) {
-      id = id_next;
-      load_tile<D>(p, regs, id, kvh, off_of(u + 1), part);
-      id_next = page_of(u + 2);
-    }
+    fetch(u + 1);
     floatx16_t sc[2];
+    const uint8_t* k_at = lds.k[buf] + Lds::at(l32) + 16 * h;
+    sc[0] = sc[1] = (floatx16_t)(0.0f);
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-      sc[kt] = (floatx16_t)(0.0f);
-      const uint8_t* at = lds.k[buf] + Lds::at(32 * kt + l32) + 16 * h;
+    for (int w = 0; w < kSteps; ++w)
 #pragma unroll
-      for (int w = 0; w < kSteps; ++w)
-        sc[kt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const half8_t*>(at + 32 * w), qf[w], sc[kt],
-                                                        0, 0, 0);
-    }
+      for (int kt = 0; kt < 2; ++kt)  // two chains of products in turn
+        sc[kt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            *reinterpret_cast<const half8_t*>(k_at + 8 * kt * Lds::kRow + 32 * w), qf[w], sc[kt], 0, 0, 0);
     const uint4 dead = *reinterpret_cast<const uint4*>(lds.dead[buf]);
     if (kb < all_lo || kb + kTileKeys > all_hi || (dead.x | dead.y | dead.z | dead.w)) {
 #pragma unroll
@@ -339,7 +347,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
           const int k = 32 * kt + 8 * (v >> 2) + 4 * h + (v & 3), key = (int)kb + k;
-          sc[kt][v] = (key >= see_lo && key < see_hi && lds.live[buf][k]) ? sc[kt][v] : -INFINITY;
+          const uint32_t none = 2 * kt + (v >> 3) == 0 ? dead.x : 2 * kt + (v >> 3) == 1 ? dead.y
+                                : 2 * kt + (v >> 3) == 2 ? dead.z : dead.w;
+          sc[kt][v] = (key >= see_lo && key < see_hi && !none) ? sc[kt][v] : -INFINITY;
         }
     }
     float top = max3(sc[0][0], sc[1][0], sc[1][1]), top2 = max3(sc[0][1], sc[0][2], sc[1][2]);
@@ -377,7 +387,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams
       for (int j = 0; j < 4; ++j)
         o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(tr_pair(vt + 4 * j * Lds::kRow + 64 * i, 2 * Lds::kRow), pf[j], o[i],
                                                       0, 0, 0);
-    if (more) put(regs, id, buf ^ 1);
+    put(buf ^ 1);
     __syncthreads();
   }
 
