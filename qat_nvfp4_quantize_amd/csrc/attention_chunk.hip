@@ -12,8 +12,9 @@
 // transpose reads.  The softmax reference moves only when a score exceeds it
 // by 15 (powers of two), as in the few-rows kernel.
 //
-// Row tiles with many keys are split over workgroups where there are few of
-// them (planned on the device from cu_q and kv_len), and joined afterwards.
+// Where there are few row tiles, their key tiles are dealt to the workgroups
+// that the chip holds in equal runs (planned on the device from cu_q and
+// kv_len), and the parts of tiles that a run's end divides are joined.
 
 #include <hip/hip_runtime.h>
 
@@ -34,7 +35,7 @@ typedef short v4i16_t __attribute__((ext_vector_type(4)));
 typedef short v8i16_t __attribute__((ext_vector_type(8)));
 #define NVQ_LDS __attribute__((address_space(3)))
 
-constexpr int kTileRows = 128, kTileKeys = 64;
+constexpr int kTileKeys = 64;
 constexpr float kRefRoom = 15, kRefStart = 9;  // as in the few-rows kernel
 
 // Keys of row tile qt of sequence s, in 64-key tiles from `base`.
@@ -42,9 +43,9 @@ struct TileRange {
   int64_t base, hi;
   int units;
 };
-__device__ __forceinline__ TileRange tile_range(const AttnParams& p, const Seq& s, int qt) {
-  const int i0 = (int)((int64_t)qt * kTileRows / p.g);
-  const int i1 = min(s.n - 1, (int)(((int64_t)(qt + 1) * kTileRows - 1) / p.g));
+__device__ __forceinline__ TileRange tile_range(const AttnParams& p, const Seq& s, int qt, int tile_rows) {
+  const int i0 = (int)((int64_t)qt * tile_rows / p.g);
+  const int i1 = min(s.n - 1, (int)(((int64_t)(qt + 1) * tile_rows - 1) / p.g));
   TileRange r;
   int64_t lo, x;
   visible(p, s, s.pos0 + i0, lo, x);
@@ -54,21 +55,19 @@ __device__ __forceinline__ TileRange tile_range(const AttnParams& p, const Seq& 
   return r;
 }
 
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* s_wave) {
-#pragma unroll
-  for (int x = 1; x < 64; x <<= 1) v += __shfl_xor(v, x, 64);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) s_wave[threadIdx.x >> 6] = v;
-  __syncthreads();
-  int64_t sum = 0;
-  for (int w = 0; w < (int)blockDim.x >> 6; ++w) sum += s_wave[w];
-  return sum;
-}
+constexpr int kMinUnits = 4;  // key tiles of a run, where there are so many
+// With this many row tiles per place they go out whole, the ones with most
+// keys first; with fewer the units are dealt in equal runs, which costs a
+// second pass over the divided tiles.
+constexpr float kWholeTiles = 1.5f;
+
+// Workgroups of a kernel variant that a CU holds.
+constexpr int chunk_wgs_per_cu(int D, int W) { return W == 8 || D == 256 ? 1 : D == 128 ? 2 : 3; }
 
 // One workgroup plans the call: the row tiles of the sequences (the last rows,
-// which see the most keys, first), their pieces, and the list of split tiles.
+// which see the most keys, first), the units up to each, and the cuts.
 __global__ __launch_bounds__(1024) void k_attn_chunk_plan(AttnParams p, ChunkPlan plan) {
-  __shared__ int64_t s_sum[16];
+  __shared__ int s_end[1024];  // tile_end of the first 1024 sequences
   __shared__ int s_scan[16];
   __shared__ int s_last;
   const int t = threadIdx.x;
@@ -84,52 +83,60 @@ __global__ __launch_bounds__(1024) void k_attn_chunk_plan(AttnParams p, ChunkPla
     if (b0 + t < p.B) {
       const Seq s = load_seq(p, b0 + t);
       const int64_t rows = (int64_t)s.n * p.g;
-      n = rows > plan.min_rows ? (int)((rows + kTileRows - 1) / kTileRows) : 0;
+      n = rows > plan.min_rows ? (int)((rows + plan.tile_rows - 1) / plan.tile_rows) : 0;
     }
     const int incl = block_inclusive_scan(n, s_scan);
+    if (b0 == 0) s_end[t] = incl;
     if (b0 + t < p.B) plan.tile_end[b0 + t] = tiles + incl;
     tiles += last(incl);
   }
-  tiles = min<int64_t>(tiles, plan.max_tiles);  // overlapping row ranges could name more
+  tiles = (int)min<int64_t>(tiles, plan.max_tiles);  // overlapping row ranges could name more
   __threadfence_block();
   __syncthreads();
-  auto tile_at = [&](int i, int& b, int& qt) {
-    int lo = 0, hi = p.B - 1;
+  auto end_of = [&](int b) { return b < 1024 ? s_end[b] : plan.tile_end[b]; };
+  int64_t total = 0;
+  for (int i0 = 0; i0 < tiles; i0 += 1024) {
+    const int i = i0 + t;
+    int units = 0;
+    if (i < tiles) {
+      int lo = 0, hi = p.B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (end_of(mid) > i)
+          hi = mid;
+        else
+          lo = mid + 1;
+      }
+      const int qt = end_of(lo) - 1 - i;
+      units = tile_range(p, load_seq(p, lo), qt, plan.tile_rows).units;
+      plan.tile[i] = make_int2(lo, qt);
+    }
+    const int incl = block_inclusive_scan(units, s_scan);
+    if (i < tiles) plan.unit_end[i] = total + incl;
+    total += last(incl);
+  }
+  const int64_t workers = max<int64_t>(1, min<int64_t>(plan.workers, total / kMinUnits));
+  const bool divide = (float)tiles < kWholeTiles * (float)workers && workers > 1;
+  if (t == 0) {
+    plan.info[0] = divide ? workers : tiles;
+    plan.info[1] = divide;
+    plan.info[2] = total;
+  }
+  if (!divide) return;
+  __threadfence_block();
+  __syncthreads();
+  for (int64_t w = t; w < workers; w += 1024) {
+    const int64_t x = w * total / workers;
+    int lo = 0, hi = tiles - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (plan.tile_end[mid] > i)
+      if (plan.unit_end[mid] > x)
         hi = mid;
       else
         lo = mid + 1;
     }
-    b = lo;
-    qt = plan.tile_end[lo] - 1 - i;
-    return tile_range(p, load_seq(p, lo), qt).units;
-  };
-  int64_t total = 0;
-  for (int i = t; i < tiles; i += 1024) {
-    int b, qt;
-    total += tile_at(i, b, qt);
+    plan.run_tile[w] = lo;
   }
-  total = block_sum(total, s_sum);
-  const int64_t per = max<int64_t>((total * p.c.H + plan.target - 1) / plan.target, plan.min_units);
-  int items = 0, slots = 0, splits = 0;
-  for (int i0 = 0; i0 < tiles; i0 += 1024) {
-    int b = 0, qt = 0, n = 0;
-    if (i0 + t < tiles) n = (int)((tile_at(i0 + t, b, qt) + per - 1) / per);
-    const int split = n > 1;
-    const int incl = block_inclusive_scan(n, s_scan);
-    const int all = last(incl);
-    const int incl_slot = block_inclusive_scan(split ? n : 0, s_scan);
-    const int all_slot = last(incl_slot);
-    const int incl_split = block_inclusive_scan(split, s_scan);
-    const int all_split = last(incl_split);
-    for (int k = 0; k < n; ++k)
-      plan.item[items + incl - n + k] = make_int4(b, qt, k << 16 | n, slots + incl_slot - n + k);
-    if (split) plan.split[splits + incl_split - 1] = make_int4(b, qt, n, slots + incl_slot - n);
-    items += all, slots += all_slot, splits += all_split;
-  }
-  if (t == 0) plan.count[0] = items, plan.count[1] = splits;
 }
 
 // Two transpose reads -> the 8 keys of one element of an A operand: in each
@@ -142,45 +149,53 @@ __device__ __forceinline__ half8_t tr_pair(const NVQ_LDS char* at, int second) {
   return __builtin_bit_cast(half8_t, v);
 }
 
-// Codes and scales of a quarter of one key's elements, K and V.
-template <int D>
+// Codes and scales of one thread's share of a tile: 1 / P of the elements of
+// one key, K and V (P = 4 with 4 waves, 8 with 8).
+template <int D, int P>
 struct TileRegs {
-  uint32_t k[D / 32], v[D / 32], ks[D / 128], vs[D / 64];
-};
-template <>
-struct TileRegs<64> {
-  uint32_t k[2], v[2], ks, vs;
+  static constexpr int kWords = D / 8 / P;                     // code dwords
+  static constexpr int kScales = D / 16 / P > 1 ? D / 16 / P : 1;
+  uint32_t k[kWords], v[kWords], ks[kScales], vs[kScales];
 };
 
-// A wave loads 16 keys of a tile, which lie in one page: its base is uniform,
-// and a lane's offsets in it (key16 of the 16 keys, quarter `part` of the
-// elements) never change.  id < 0 (no such page) reads page 0, masked later.
-template <int D>
-__device__ __forceinline__ void load_tile(const AttnParams& p, TileRegs<D>& r, int id, int kvh, int off,
-                                          uint32_t key16, uint32_t part) {
+// A wave loads 64 / P keys of a tile, which lie in one page: its base is
+// uniform, and a lane's offsets in it (key `key` of these, share `part`) never
+// change.  id < 0 (no such page) reads page 0, masked later.  Shares of 32
+// elements and more are pieces of 32, 32 P apart.
+template <int D, int P>
+__device__ __forceinline__ void load_tile(const AttnParams& p, TileRegs<D, P>& r, int id, int kvh, int off,
+                                          uint32_t key, uint32_t part) {
+  constexpr int kWords = TileRegs<D, P>::kWords;
   const int64_t tile = ((int64_t)max(id, 0) * p.c.H + kvh) << p.c.log_ps;
   const uint8_t* kc = p.c.k_codes + (tile + off) * (D / 2);
   const uint8_t* vc = p.c.v_codes + (tile + off) * (D / 2);
   const uint8_t* ks = p.c.k_scales + (tile + off) * (D / 16);
   const uint8_t* vs = p.c.v_scales + tile * (D / 16) + off;
-  const uint32_t at = key16 * (D / 2), sat = key16 * (D / 16);
-  if constexpr (D == 64) {
-    const uint2 x = *reinterpret_cast<const uint2*>(kc + (at + 8 * part));
-    const uint2 y = *reinterpret_cast<const uint2*>(vc + (at + 8 * part));
-    r.k[0] = x.x, r.k[1] = x.y, r.v[0] = y.x, r.v[1] = y.y;
-    r.ks = ks[sat + part];
-    r.vs = vs[key16 + (part << p.c.log_ps)];
-  } else {
+  const uint32_t at = key * (D / 2), sat = key * (D / 16);
+  if constexpr (kWords >= 4) {
 #pragma unroll
-    for (int i = 0; i < D / 128; ++i) {
-      const uint4 x = *reinterpret_cast<const uint4*>(kc + (at + 16 * part) + 64 * i);
-      const uint4 y = *reinterpret_cast<const uint4*>(vc + (at + 16 * part) + 64 * i);
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4*>(kc + (at + 16 * part) + 16 * P * i);
+      const uint4 y = *reinterpret_cast<const uint4*>(vc + (at + 16 * part) + 16 * P * i);
       r.k[4 * i] = x.x, r.k[4 * i + 1] = x.y, r.k[4 * i + 2] = x.z, r.k[4 * i + 3] = x.w;
       r.v[4 * i] = y.x, r.v[4 * i + 1] = y.y, r.v[4 * i + 2] = y.z, r.v[4 * i + 3] = y.w;
-      r.ks[i] = *reinterpret_cast<const uint16_t*>(ks + (sat + 2 * part) + 8 * i);
-      r.vs[2 * i] = vs[key16 + ((8 * i + 2 * part) << p.c.log_ps)];
-      r.vs[2 * i + 1] = vs[key16 + ((8 * i + 2 * part + 1) << p.c.log_ps)];
+      const uint32_t two = *reinterpret_cast<const uint16_t*>(ks + (sat + 2 * part) + 2 * P * i);
+      r.ks[2 * i] = two, r.ks[2 * i + 1] = two >> 8;
+      r.vs[2 * i] = vs[key + ((2 * P * i + 2 * part) << p.c.log_ps)];
+      r.vs[2 * i + 1] = vs[key + ((2 * P * i + 2 * part + 1) << p.c.log_ps)];
     }
+  } else {
+    if constexpr (kWords == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(kc + (at + 8 * part));
+      const uint2 y = *reinterpret_cast<const uint2*>(vc + (at + 8 * part));
+      r.k[0] = x.x, r.k[1] = x.y, r.v[0] = y.x, r.v[1] = y.y;
+    } else {
+      r.k[0] = *reinterpret_cast<const uint32_t*>(kc + (at + 4 * part));
+      r.v[0] = *reinterpret_cast<const uint32_t*>(vc + (at + 4 * part));
+    }
+    const uint32_t blk = kWords == 2 ? part : part >> 1;
+    r.ks[0] = ks[sat + blk];
+    r.vs[0] = vs[key + (blk << p.c.log_ps)];
   }
 }
 
@@ -188,18 +203,14 @@ __device__ __forceinline__ void load_tile(const AttnParams& p, TileRegs<D>& r, i
 __device__ __forceinline__ uint32_t scale_of(uint32_t byte) { return (byte & 0x7Fu) * 0x00800080u; }
 
 // Dequantizes and writes to the LDS tiles.
-template <int D>
-__device__ __forceinline__ void store_tile(const TileRegs<D>& r, uint8_t* k, uint8_t* v, int part) {
+template <int D, int P>
+__device__ __forceinline__ void store_tile(const TileRegs<D, P>& r, uint8_t* k, uint8_t* v, int part) {
+  constexpr int kWords = TileRegs<D, P>::kWords, kPiece = kWords < 4 ? kWords : 4;
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j) {
-    const int at = D == 64 ? 32 * part + 16 * j : 256 * (j >> 2) + 64 * part + 16 * (j & 3);
-    uint32_t ks, vs;
-    if constexpr (D == 64)
-      ks = scale_of(r.ks), vs = scale_of(r.vs);
-    else
-      ks = scale_of((j >> 1) & 1 ? r.ks[j >> 2] >> 8 : r.ks[j >> 2]), vs = scale_of(r.vs[j >> 1]);
-    *reinterpret_cast<half8_t*>(k + at) = dequant8(r.k[j], ks);
-    *reinterpret_cast<half8_t*>(v + at) = dequant8(r.v[j], vs);
+  for (int j = 0; j < kWords; ++j) {
+    const int at = 16 * (kPiece * (P * (j / kPiece) + part) + j % kPiece);
+    *reinterpret_cast<half8_t*>(k + at) = dequant8(r.k[j], scale_of(r.ks[j >> 1]));
+    *reinterpret_cast<half8_t*>(v + at) = dequant8(r.v[j], scale_of(r.vs[j >> 1]));
   }
 }
 
@@ -226,26 +237,45 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return m;
 }
 
-template <int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams p, ChunkPlan plan) {
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, chunk_wgs_per_cu(D, W) * W / 4) void k_attn_chunk(AttnParams p, ChunkPlan plan) {
   using Lds = ChunkLds<D>;
-  constexpr int kSteps = D / 16, kOut = D / 32;
+  constexpr int kSteps = D / 16, kOut = D / 32, kTileRows = 32 * W;
   __shared__ Lds lds;
   if (plan.check && blockIdx.x == 0) {
-    check_batch(p, reinterpret_cast<CheckLds&>(lds));
+    if (threadIdx.x < 256) check_batch(p, reinterpret_cast<CheckLds&>(lds));
     return;
   }
-  const int block = blockIdx.x - plan.check, kvh = block % p.c.H, item = block / p.c.H;
-  if (item >= plan.count[0]) return;
-  const int4 it = plan.item[item];
-  const int b = __builtin_amdgcn_readfirstlane(it.x), qt = __builtin_amdgcn_readfirstlane(it.y);
-  const int index = __builtin_amdgcn_readfirstlane(it.z) >> 16, count = __builtin_amdgcn_readfirstlane(it.z) & 0xFFFF;
-  const Seq s = load_seq(p, b);
-  const TileRange range = tile_range(p, s, qt);
-  const int u_begin = (int)((int64_t)index * range.units / count);
-  const int u_end = (int)((int64_t)(index + 1) * range.units / count);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int block = blockIdx.x - plan.check, kvh = block % p.c.H, run = block / p.c.H;
+  if (run >= plan.info[0]) return;
+  const bool divide = plan.info[1] != 0;
+  int tile = run;
+  int64_t x, x_end;
+  if (divide) {
+    tile = __builtin_amdgcn_readfirstlane(plan.run_tile[run]);
+    x = run * plan.info[2] / plan.info[0], x_end = (run + 1) * plan.info[2] / plan.info[0];
+  } else {
+    x = tile ? plan.unit_end[tile - 1] : 0, x_end = plan.unit_end[tile];
+  }
+  const int64_t x_begin = x;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float v_st = *p.c.v_st, k_factor = p.scale_log2 * *p.c.k_st;
+
+#pragma unroll 1
+  for (; x < x_end; ++tile) {
+  // made anew for each tile, as in the few-rows kernel
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
   const int l32 = lane & 31, h = lane >> 5;
+  const int b = __builtin_amdgcn_readfirstlane(plan.tile[tile].x), qt = __builtin_amdgcn_readfirstlane(plan.tile[tile].y);
+  const Seq s = load_seq(p, b);
+  const TileRange range = tile_range(p, s, qt, kTileRows);
+  const int64_t tile_x = plan.unit_end[tile] - range.units;  // its first unit
+  const int u_begin = (int)(x - tile_x), u_end = (int)min<int64_t>(range.units, x_end - tile_x);
+  // slot 0: the part that starts a run; 1: one that ends it and began within
+  const bool whole = u_begin == 0 && u_end == range.units;
+  const int64_t slot = 2 * (int64_t)run + (x != x_begin);
+  x = tile_x + u_end;
   const int32_t* table = p.table + b * p.table_ld;
 
   // this lane's query row
@@ -269,7 +299,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams
     // the largest product is the largest score, and a factor of 0 too
     const int ex = (int)(top >> 23);
     const int shift = (top == 0u || ex == 255) ? 0 : 14 + 127 - max(ex, 1);
-    const float c0 = __builtin_ldexpf(p.scale_log2 * *p.c.k_st, -shift);
+    const float c0 = __builtin_ldexpf(k_factor, -shift);
     const float sign = c0 < 0.0f ? -1.0f : c0 > 0.0f ? 1.0f : 0.0f;
     cq = c0 == 0.0f ? 1.0f : fabsf(c0);
 #pragma unroll
@@ -294,29 +324,30 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams
   for (int i = 0; i < kOut; ++i) o[i] = (floatx16_t)(0.0f);
   float ref = -INFINITY, ref_safe = 0.0f, l = 0.0f;
 
-  // Loader: a wave takes 16 keys of the tile, a thread a quarter of one of
-  // them, 16 lanes keys 4 apart.  Page ids of the wave's next 64 tiles with one
-  // load (-1: no key, or an id outside the cache).
-  const int part = threadIdx.x & 3, key16 = 4 * ((lane >> 2) & 3) + (lane >> 4);
-  const int lkey_at = Lds::at(16 * wave + key16);
-  const int64_t base = range.base + 16 * wave;
+  // Loader: a wave takes 64 / W keys of the tile, a thread 1 / W of one of
+  // them, the 16 lanes of an LDS access keys 4 apart.  Page ids of the wave's
+  // next 64 tiles with one load (-1: no key, or an id outside the cache).
+  const int part = lane & (W - 1);
+  const int key = W == 4 ? 4 * ((lane >> 2) & 3) + (lane >> 4) : 4 * ((lane >> 3) & 1) + (lane >> 4);
+  const int lkey_at = Lds::at(64 / W * wave + key);
+  const int64_t base = range.base + 64 / W * wave;
   int ids = -1, ids_at = u_begin;
   auto fetch_ids = [&](int u0) {
-    const int64_t key = base + (int64_t)(u0 + lane) * kTileKeys;
-    const int id = (u0 + lane < u_end && key < range.hi) ? table[key >> p.c.log_ps] : -1;
+    const int64_t first = base + (int64_t)(u0 + lane) * kTileKeys;
+    const int id = (u0 + lane < u_end && first < range.hi) ? table[first >> p.c.log_ps] : -1;
     ids = id < p.c.num_pages ? id : -1;
     ids_at = u0;
   };
-  TileRegs<D> regs;
+  TileRegs<D, W> regs;
   int id;
   auto fetch = [&](int u) {  // past the last tile: page 0, never looked at
     if (u - ids_at >= 64) fetch_ids(u);
     id = __builtin_amdgcn_readlane(ids, u - ids_at);
-    load_tile<D>(p, regs, id, kvh, (int)(base + (int64_t)u * kTileKeys) & (p.c.ps - 1), key16, part);
+    load_tile<D, W>(p, regs, id, kvh, (int)(base + (int64_t)u * kTileKeys) & (p.c.ps - 1), key, part);
   };
   auto put = [&](int buf) {
-    store_tile<D>(regs, lds.k[buf] + lkey_at, lds.v[buf] + lkey_at, part);
-    if (lane == 0) lds.dead[buf][wave] = id < 0;
+    store_tile<D, W>(regs, lds.k[buf] + lkey_at, lds.v[buf] + lkey_at, part);
+    if (lane == 0 && wave % (W / 4) == 0) lds.dead[buf][wave / (W / 4)] = id < 0;
   };
   fetch_ids(u_begin);
   fetch(u_begin);
@@ -334,12 +365,25 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams
     floatx16_t sc[2];
     const uint8_t* k_at = lds.k[buf] + Lds::at(l32) + 16 * h;
     sc[0] = sc[1] = (floatx16_t)(0.0f);
+    // Operands of the next two steps are read before the products of these:
+    // left alone the compiler puts each read right before its product and
+    // waits for it.
+    half8_t kf[2][4];
+    auto read_k = [&](half8_t (&f)[4], int w) {
 #pragma unroll
-    for (int w = 0; w < kSteps; ++w)
+      for (int i = 0; i < 4; ++i)
+        f[i] = *reinterpret_cast<const half8_t*>(k_at + 8 * (i & 1) * Lds::kRow + 32 * (w + (i >> 1)));
+    };
+    read_k(kf[0], 0);
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt)  // two chains of products in turn
-        sc[kt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-            *reinterpret_cast<const half8_t*>(k_at + 8 * kt * Lds::kRow + 32 * w), qf[w], sc[kt], 0, 0, 0);
+    for (int w = 0; w < kSteps; w += 2) {
+      if (w + 2 < kSteps) read_k(kf[(w >> 1 & 1) ^ 1], w + 2);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // two chains of products in turn
+        sc[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[w >> 1 & 1][i], qf[w + (i >> 1)], sc[i & 1], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     const uint4 dead = *reinterpret_cast<const uint4*>(lds.dead[buf]);
     if (kb < all_lo || kb + kTileKeys > all_hi || (dead.x | dead.y | dead.z | dead.w)) {
 #pragma unroll
@@ -371,104 +415,154 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_chunk(AttnParams
 #pragma unroll
       for (int i = 0; i < kOut; ++i) o[i] *= keep;
     }
-    half8_t pf[4];
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[kt][v], cq, -ref_safe));
-        l += w;
-        pf[2 * kt + (v >> 3)][v & 7] = (_Float16)w;
-      }
     const NVQ_LDS char* vt = (const NVQ_LDS char*)lds.v[buf] + tr_off;
+    half8_t vf[2][kOut], pf[2];
+    auto read_v = [&](half8_t (&f)[kOut], int j) {
 #pragma unroll
-    for (int i = 0; i < kOut; ++i)
+      for (int i = 0; i < kOut; ++i) f[i] = tr_pair(vt + 4 * j * Lds::kRow + 64 * i, 2 * Lds::kRow);
+    };
+    auto weights = [&](half8_t& f, int j) {  // of 16 keys
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(tr_pair(vt + 4 * j * Lds::kRow + 64 * i, 2 * Lds::kRow), pf[j], o[i],
-                                                      0, 0, 0);
-    put(buf ^ 1);
+      for (int v = 0; v < 8; ++v) {
+        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j >> 1][8 * (j & 1) + v], cq, -ref_safe));
+        l += w;
+        f[v] = (_Float16)w;
+      }
+    };
+    read_v(vf[0], 0);
+    weights(pf[0], 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j < 3) read_v(vf[(j & 1) ^ 1], j + 1);
+      if (j < 3)
+        weights(pf[(j & 1) ^ 1], j + 1);
+      else
+        put(buf ^ 1);
+#pragma unroll
+      for (int i = 0; i < kOut; ++i)
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[j & 1][i], pf[j & 1], o[i], 0, 0, 0);
+    }
     __syncthreads();
   }
 
   l += __shfl_xor(l, 32, 64);
-  if (count == 1) {
-    if (!live) return;
-    const float inv = l == 0.0f ? 0.0f : *p.c.v_st / l;
-    uint16_t* out = p.out + (s.row0 + qi) * p.out_ld_t + qh * p.out_ld_h;
+  if (whole) {
+    if (live) {
+      const float inv = l == 0.0f ? 0.0f : v_st / l;
+      uint16_t* out = p.out + (s.row0 + qi) * p.out_ld_t + qh * p.out_ld_h;
 #pragma unroll
-    for (int i = 0; i < kOut; ++i)
+      for (int i = 0; i < kOut; ++i)
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        *reinterpret_cast<uint2*>(out + 32 * i + 8 * v + 4 * h) =
-            make_uint2(f32_to_bf16_any(o[i][4 * v] * inv) | (f32_to_bf16_any(o[i][4 * v + 1] * inv) << 16),
-                       f32_to_bf16_any(o[i][4 * v + 2] * inv) | (f32_to_bf16_any(o[i][4 * v + 3] * inv) << 16));
-    if (p.lse && h == 0)
-      p.lse[(int64_t)(s.row0 + qi) * p.Hq + qh] = l == 0.0f ? -INFINITY : (ref + __builtin_log2f(l)) * kLn2;
+        for (int v = 0; v < 4; ++v)
+          *reinterpret_cast<uint2*>(out + 32 * i + 8 * v + 4 * h) =
+              make_uint2(f32_to_bf16_any(o[i][4 * v] * inv) | (f32_to_bf16_any(o[i][4 * v + 1] * inv) << 16),
+                         f32_to_bf16_any(o[i][4 * v + 2] * inv) | (f32_to_bf16_any(o[i][4 * v + 3] * inv) << 16));
+      if (p.lse && h == 0)
+        p.lse[(int64_t)(s.row0 + qi) * p.Hq + qh] = l == 0.0f ? -INFINITY : (ref + __builtin_log2f(l)) * kLn2;
+    }
   } else {
-    const int64_t slot = ((int64_t)__builtin_amdgcn_readfirstlane(it.w) * p.c.H + kvh) * kTileRows + 32 * wave + l32;
-    float* out = plan.part_o + slot * D;
+    const int64_t at = (slot * p.c.H + kvh) * kTileRows + 32 * wave + l32;
+    float* out = plan.part_o + at * D;
 #pragma unroll
     for (int i = 0; i < kOut; ++i)
 #pragma unroll
       for (int v = 0; v < 4; ++v)
         *reinterpret_cast<float4*>(out + 32 * i + 8 * v + 4 * h) =
             make_float4(o[i][4 * v], o[i][4 * v + 1], o[i][4 * v + 2], o[i][4 * v + 3]);
-    if (h == 0) plan.part_ml[slot] = make_float2(ref, l);
+    if (h == 0) plan.part_ml[at] = make_float2(ref, l);
+  }
   }
 }
 
-// Joins the pieces of the split row tiles: a wave per row, a lane D / 64
-// elements; the workgroups walk the (tile, head, 4 rows) list.
+// Joins the parts of the divided tiles: a workgroup per cut, key/value head
+// and 4 rows takes the tile if the cut is the first in it; its waves take
+// parts in turn (a long context has one for every workgroup), a lane D / 64
+// elements of each row.
+constexpr int kJoinRows = 4;
+
 template <int D>
 __global__ __launch_bounds__(256) void k_attn_chunk_join(AttnParams p, ChunkPlan plan) {
   constexpr int kE = D / 64;
+  __shared__ float s_o[4][kJoinRows][D];
+  __shared__ float s_m[4][kJoinRows], s_l[4][kJoinRows];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int64_t todo = (int64_t)plan.count[1] * p.c.H * (kTileRows / 4);
-  for (int64_t w = blockIdx.x; w < todo; w += gridDim.x) {
-    const int rr = (int)(w % (kTileRows / 4)) * 4 + wave;
-    const int64_t th = w / (kTileRows / 4);
-    const int kvh = (int)(th % p.c.H);
-    const int4 it = plan.split[th / p.c.H];
-    const Seq s = load_seq(p, it.x);
-    const int64_t r = (int64_t)it.y * kTileRows + rr;
-    if (r >= (int64_t)s.n * p.g) continue;
-    auto slot = [&](int i) { return ((int64_t)(it.w + i) * p.c.H + kvh) * kTileRows + rr; };
-    float m = -INFINITY;
-    for (int i = lane; i < it.z; i += 64) m = fmaxf(m, plan.part_ml[slot(i)].x);
+  const int kvh = blockIdx.y;
+  const int64_t w = blockIdx.x + 1, runs = plan.info[0], total = plan.info[2];
+  if (plan.info[1] == 0 || w >= runs) return;
+  const int tile = plan.run_tile[w];
+  const int2 bq = plan.tile[tile];
+  const int64_t end = plan.unit_end[tile], start = tile ? plan.unit_end[tile - 1] : 0;
+  const int64_t cut = w * total / runs, before = (w - 1) * total / runs;
+  if (cut == start || before > start) return;
+  const int64_t first = 2 * (w - 1) + (before != start);
+  const int count = (int)((end * runs - 1) / total - (w - 1)) + 1;
+  const Seq s = load_seq(p, bq.x);
+  const int64_t r0 = (int64_t)bq.y * plan.tile_rows + blockIdx.z * kJoinRows, rows = (int64_t)s.n * p.g;
+  if (r0 < 0 || r0 >= rows) return;
+  auto at = [&](int i) {  // row r0 of part i
+    return ((i == 0 ? first : 2 * (w - 1 + i)) * p.c.H + kvh) * plan.tile_rows + blockIdx.z * kJoinRows;
+  };
+  float m[kJoinRows], l[kJoinRows], o[kJoinRows][kE];
 #pragma unroll
-    for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x, 64));
-    const float ref = m == -INFINITY ? 0.0f : m;
-    float o[kE], l = 0.0f;
+  for (int k = 0; k < kJoinRows; ++k) {
+    m[k] = -INFINITY, l[k] = 0.0f;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < it.z; ++i) {
-      const float2 ml = plan.part_ml[slot(i)];
-      const float f = __builtin_amdgcn_exp2f(ml.x - ref);
-      l += ml.y * f;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) o[e] += plan.part_o[slot(i) * D + kE * lane + e] * f;
-    }
-    const int qi = (int)(r / p.g), qh = kvh * p.g + (int)(r % p.g);
-    const float inv = l == 0.0f ? 0.0f : *p.c.v_st / l;
-    uint16_t* out = p.out + (s.row0 + qi) * p.out_ld_t + qh * p.out_ld_h + kE * lane;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) out[e] = (uint16_t)f32_to_bf16_any(o[e] * inv);
-    if (p.lse && lane == 0)
-      p.lse[(int64_t)(s.row0 + qi) * p.Hq + qh] = l == 0.0f ? -INFINITY : (m + __builtin_log2f(l)) * kLn2;
+    for (int e = 0; e < kE; ++e) o[k][e] = 0.0f;
   }
+#pragma unroll 2
+  for (int i = wave; i < count; i += 4)
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k) {
+      const float2 ml = plan.part_ml[at(i) + k];
+      const float top = fmaxf(m[k], ml.x), ref = top == -INFINITY ? 0.0f : top;
+      const float keep = __builtin_amdgcn_exp2f(m[k] - ref), f = __builtin_amdgcn_exp2f(ml.x - ref);
+      m[k] = top;
+      l[k] = l[k] * keep + ml.y * f;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) o[k][e] = o[k][e] * keep + plan.part_o[(at(i) + k) * D + kE * lane + e] * f;
+    }
+#pragma unroll
+  for (int k = 0; k < kJoinRows; ++k) {
+    if (lane == 0) s_m[wave][k] = m[k], s_l[wave][k] = l[k];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) s_o[wave][k][kE * lane + e] = o[k][e];
+  }
+  __syncthreads();
+  const int k = wave;  // a row per wave
+  const int64_t r = r0 + k;
+  if (r >= rows) return;
+  const float top = fmaxf(fmaxf(s_m[0][k], s_m[1][k]), fmaxf(s_m[2][k], s_m[3][k]));
+  const float ref = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f, x[kE];
+#pragma unroll
+  for (int e = 0; e < kE; ++e) x[e] = 0.0f;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const float f = __builtin_amdgcn_exp2f(s_m[v][k] - ref);
+    sum += s_l[v][k] * f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) x[e] += s_o[v][k][kE * lane + e] * f;
+  }
+  const int qi = (int)(r / p.g), qh = kvh * p.g + (int)(r % p.g);
+  const float inv = sum == 0.0f ? 0.0f : *p.c.v_st / sum;
+  uint16_t* out = p.out + (s.row0 + qi) * p.out_ld_t + qh * p.out_ld_h + kE * lane;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) out[e] = (uint16_t)f32_to_bf16_any(x[e] * inv);
+  if (p.lse && lane == 0)
+    p.lse[(int64_t)(s.row0 + qi) * p.Hq + qh] = sum == 0.0f ? -INFINITY : (top + __builtin_log2f(sum)) * kLn2;
 }
 
-template <int D>
+template <int D, int W>
 int launch_chunk(const AttnParams& p, const ChunkPlan& plan, hipStream_t s) {
   hipLaunchKernelGGL(k_attn_chunk_plan, dim3(1), dim3(1024), 0, s, p, plan);
   if (int rc = last_launch()) return rc;
-  hipLaunchKernelGGL((k_attn_chunk<D>), dim3((unsigned)(plan.max_items * p.c.H + plan.check)), dim3(256), 0, s, p,
-                     plan);
+  const int64_t runs = std::max<int64_t>(plan.max_tiles, plan.workers);
+  hipLaunchKernelGGL((k_attn_chunk<D, W>), dim3((unsigned)(runs * p.c.H + plan.check)), dim3(64 * W), 0, s, p, plan);
   if (int rc = last_launch()) return rc;
-  if (!plan.may_split) return NVQ_OK;
-  hipLaunchKernelGGL((k_attn_chunk_join<D>), dim3(2 * device_cu_count()), dim3(256), 0, s, p, plan);
+  if (plan.workers == 1) return NVQ_OK;
+  hipLaunchKernelGGL((k_attn_chunk_join<D>),
+                     dim3((unsigned)plan.workers - 1, (unsigned)p.c.H, (unsigned)(plan.tile_rows / kJoinRows)), dim3(256),
+                     0, s, p, plan);
   return last_launch();
 }
 
@@ -476,30 +570,30 @@ int launch_chunk(const AttnParams& p, const ChunkPlan& plan, hipStream_t s) {
 
 void attn_chunk_plan(const AttnParams& p, int min_rows, bool check, WsCarve& ws, ChunkPlan& plan) {
   plan.min_rows = min_rows;
-  plan.min_units = kChunkMinUnits;
-  plan.target = kChunkTarget;
   plan.check = check;
   // rows of a sequence are cut to the call's, so its tiles are at most this
-  plan.max_tiles = (int64_t)p.total_q * p.g / kTileRows + p.B;
-  const int64_t units = (p.num_keys + 2 * kTileKeys - 2) / kTileKeys;
-  plan.may_split = units > plan.min_units;
-  const int64_t by_target = (plan.target + p.c.H - 1) / p.c.H;
-  plan.max_items = plan.max_tiles + (plan.may_split ? by_target : 0);
-  plan.count = ws.take<int32_t>(2);
+  const int waves = p.c.D == 128 && (int64_t)p.max_q * p.g > 128 ? 8 : 4;
+  plan.tile_rows = 32 * waves;
+  plan.max_tiles = (int64_t)p.total_q * p.g / plan.tile_rows + p.B;
+  const int64_t units = (p.num_keys + kTileKeys - 1) / kTileKeys + 1;  // most of a tile
+  const int64_t places = (int64_t)chunk_wgs_per_cu(p.c.D, waves) * device_cu_count() - plan.check;
+  plan.workers = (int)std::max<int64_t>(1, std::min(places / p.c.H, units * plan.max_tiles / kMinUnits));
+  plan.info = ws.take<int64_t>(3);
   plan.tile_end = ws.take<int32_t>((size_t)p.B);
-  plan.item = ws.take<int4>((size_t)plan.max_items);
-  // ceil(units / per) > 1 pieces are at most 2 units / per
-  const int64_t slots = plan.may_split ? std::min(2 * by_target, plan.max_items) : 0;
-  plan.split = ws.take<int4>((size_t)slots);
-  plan.part_ml = ws.take<float2>((size_t)(slots * p.c.H * kTileRows));
-  plan.part_o = ws.take<float>((size_t)(slots * p.c.H * kTileRows * p.c.D));
+  plan.tile = ws.take<int2>((size_t)plan.max_tiles);
+  plan.unit_end = ws.take<int64_t>((size_t)plan.max_tiles);
+  plan.run_tile = ws.take<int32_t>((size_t)plan.workers);
+  const size_t rows = plan.workers > 1 ? (size_t)(2 * plan.workers * p.c.H) * plan.tile_rows : 0;
+  plan.part_ml = ws.take<float2>(rows);
+  plan.part_o = ws.take<float>(rows * p.c.D);
 }
 
 int attn_chunk_launch(const AttnParams& p, const ChunkPlan& plan, hipStream_t s) {
-  switch (p.c.D) {
-    case 64: return launch_chunk<64>(p, plan, s);
-    case 128: return launch_chunk<128>(p, plan, s);
-    default: return launch_chunk<256>(p, plan, s);
+  switch (p.c.D * 16 + plan.tile_rows / 32) {
+    case 64 * 16 + 4: return launch_chunk<64, 4>(p, plan, s);
+    case 128 * 16 + 4: return launch_chunk<128, 4>(p, plan, s);
+    case 128 * 16 + 8: return launch_chunk<128, 8>(p, plan, s);
+    default: return launch_chunk<256, 4>(p, plan, s);
   }
 }
 

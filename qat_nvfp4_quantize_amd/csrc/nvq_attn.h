@@ -40,24 +40,23 @@ int attn_rows_tiles(int D, int64_t rows);
 void attn_rows_plan(const AttnParams& p, int tiles, WsCarve& ws, RowsPlan& plan);
 int attn_rows_launch(const AttnParams& p, const RowsPlan& plan, hipStream_t s);
 
-// Plan of the many-rows kernel: row tiles of 128, their pieces, and where the
-// pieces of split tiles go.
+// Plan of the many-rows kernel: row tiles and their key tiles in one
+// row of units per key/value head, cut into runs, and where the parts of tiles
+// that a cut divides go.
 struct ChunkPlan {
-  int min_rows;   // sequences with no more rows per key/value head are left out
-  int min_units;  // smallest piece, in 64-key tiles
-  int target;     // pieces times heads aimed at
-  int check;      // the launch checks the index arrays
-  int may_split;
-  int64_t max_tiles, max_items;
-  int32_t* count;     // items, split tiles
-  int32_t* tile_end;  // [B] row tiles up to and with sequence b
-  int4* item;         // sequence, row tile, piece << 16 | pieces, slot
-  int4* split;        // sequence, row tile, pieces, first slot
-  float2* part_ml;    // [slot][head][128] reference and sum
-  float* part_o;      // [slot][head][128][D]
+  int min_rows;  // sequences with no more rows per key/value head are left out
+  int check;     // the launch checks the index arrays
+  int workers;   // runs per key/value head where tiles are divided
+  int tile_rows;  // 128 or 256
+  int64_t max_tiles;
+  int32_t* tile_end;   // [B] row tiles up to and with sequence b
+  int2* tile;          // [max_tiles] sequence, row tile in it
+  int64_t* unit_end;   // [max_tiles] units up to and with a tile
+  int32_t* run_tile;   // [workers] tile of a run's first unit
+  int64_t* info;       // runs, whether tiles are divided, units in all
+  float2* part_ml;     // [run][2 slots][head][tile_rows] reference and sum
+  float* part_o;       // [run][2 slots][head][tile_rows][D]
 };
-constexpr int kChunkMinUnits = 8;
-constexpr int kChunkTarget = 512;
 
 void attn_chunk_plan(const AttnParams& p, int min_rows, bool check, WsCarve& ws, ChunkPlan& plan);
 int attn_chunk_launch(const AttnParams& p, const ChunkPlan& plan, hipStream_t s);
