@@ -183,7 +183,7 @@ Plan attn_plan(const AttnParams& p, void* ws) {
     plan.use_chunk = tiles == 0;
     if (plan.use_chunk && p.B > 1) tiles = attn_rows_tiles(p.c.D, p.g);  // single tokens beside the chunks
     plan.use_rows = tiles > 0;
-    if (plan.use_rows) attn_rows_plan(p, tiles, c, plan.rows);
+    if (plan.use_rows) attn_rows_plan(p, tiles, plan.use_chunk, c, plan.rows);
     if (plan.use_chunk) attn_chunk_plan(p, 16 * tiles, !plan.use_rows, c, plan.chunk);
   }
   plan.bytes = c.off;
@@ -238,10 +238,13 @@ extern "C" int nvq_paged_attention(const nvq_kv_cache* cache, const nvq_paged_at
   p.cu_q = a.cu_q, p.kv_len = a.kv_len, p.table = a.block_table;
   p.window = a.window, p.causal = a.causal;
   p.scale_log2 = a.softmax_scale * 1.44269504088896340736f;
-  if (plan.use_rows)
-    if (int rc = attn_rows_launch(p, plan.rows, s)) return rc;
-  if (plan.use_chunk) return attn_chunk_launch(p, plan.chunk, s);
-  if (plan.use_rows) return NVQ_OK;
+  if (plan.use_rows || plan.use_chunk) {
+    if (plan.use_rows)
+      if (int rc = attn_rows_launch(p, plan.rows, plan.chunk, s)) return rc;
+    if (plan.use_chunk)
+      if (int rc = attn_chunk_launch(p, plan.chunk, plan.use_rows, s)) return rc;
+    return attn_join_launch(p, plan.use_rows ? &plan.rows : nullptr, plan.use_chunk ? &plan.chunk : nullptr, s);
+  }
   hipLaunchKernelGGL(k_attn_any, dim3((unsigned)p.total_q, (unsigned)p.Hq + 1), dim3(256), 0, s, p);
   return last_launch();
 }

@@ -22,6 +22,7 @@
 
 #include "nvq.h"
 #include "nvq_attn.h"
+#include "nvq_attn_plan.h"
 #include "nvq_dequant.h"
 #include "nvq_device.h"
 #include "nvq_internal.h"
@@ -35,109 +36,10 @@ typedef short v4i16_t __attribute__((ext_vector_type(4)));
 typedef short v8i16_t __attribute__((ext_vector_type(8)));
 #define NVQ_LDS __attribute__((address_space(3)))
 
-constexpr int kTileKeys = 64;
 constexpr float kRefRoom = 15, kRefStart = 9;  // as in the few-rows kernel
-
-// Keys of row tile qt of sequence s, in 64-key tiles from `base`.
-struct TileRange {
-  int64_t base, hi;
-  int units;
-};
-__device__ __forceinline__ TileRange tile_range(const AttnParams& p, const Seq& s, int qt, int tile_rows) {
-  const int i0 = (int)((int64_t)qt * tile_rows / p.g);
-  const int i1 = min(s.n - 1, (int)(((int64_t)(qt + 1) * tile_rows - 1) / p.g));
-  TileRange r;
-  int64_t lo, x;
-  visible(p, s, s.pos0 + i0, lo, x);
-  visible(p, s, s.pos0 + i1, x, r.hi);
-  r.base = lo & ~(int64_t)(kTileKeys - 1);
-  r.units = r.hi > r.base ? (int)((r.hi - r.base + kTileKeys - 1) / kTileKeys) : 1;
-  return r;
-}
-
-constexpr int kMinUnits = 4;  // key tiles of a run, where there are so many
-// With this many row tiles per place they go out whole, the ones with most
-// keys first; with fewer the units are dealt in equal runs, which costs a
-// second pass over the divided tiles.
-constexpr float kWholeTiles = 1.5f;
 
 // Workgroups of a kernel variant that a CU holds.
 constexpr int chunk_wgs_per_cu(int D, int W) { return W == 8 || D == 256 ? 1 : D == 128 ? 2 : 3; }
-
-// One workgroup plans the call: the row tiles of the sequences (the last rows,
-// which see the most keys, first), the units up to each, and the cuts.
-__global__ __launch_bounds__(1024) void k_attn_chunk_plan(AttnParams p, ChunkPlan plan) {
-  __shared__ int s_end[1024];  // tile_end of the first 1024 sequences
-  __shared__ int s_scan[16];
-  __shared__ int s_last;
-  const int t = threadIdx.x;
-  auto last = [&](int incl) {  // the workgroup's total of an inclusive scan
-    __syncthreads();
-    if (t == 1023) s_last = incl;
-    __syncthreads();
-    return s_last;
-  };
-  int tiles = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 1024) {
-    int n = 0;
-    if (b0 + t < p.B) {
-      const Seq s = load_seq(p, b0 + t);
-      const int64_t rows = (int64_t)s.n * p.g;
-      n = rows > plan.min_rows ? (int)((rows + plan.tile_rows - 1) / plan.tile_rows) : 0;
-    }
-    const int incl = block_inclusive_scan(n, s_scan);
-    if (b0 == 0) s_end[t] = incl;
-    if (b0 + t < p.B) plan.tile_end[b0 + t] = tiles + incl;
-    tiles += last(incl);
-  }
-  tiles = (int)min<int64_t>(tiles, plan.max_tiles);  // overlapping row ranges could name more
-  __threadfence_block();
-  __syncthreads();
-  auto end_of = [&](int b) { return b < 1024 ? s_end[b] : plan.tile_end[b]; };
-  int64_t total = 0;
-  for (int i0 = 0; i0 < tiles; i0 += 1024) {
-    const int i = i0 + t;
-    int units = 0;
-    if (i < tiles) {
-      int lo = 0, hi = p.B - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (end_of(mid) > i)
-          hi = mid;
-        else
-          lo = mid + 1;
-      }
-      const int qt = end_of(lo) - 1 - i;
-      units = tile_range(p, load_seq(p, lo), qt, plan.tile_rows).units;
-      plan.tile[i] = make_int2(lo, qt);
-    }
-    const int incl = block_inclusive_scan(units, s_scan);
-    if (i < tiles) plan.unit_end[i] = total + incl;
-    total += last(incl);
-  }
-  const int64_t workers = max<int64_t>(1, min<int64_t>(plan.workers, total / kMinUnits));
-  const bool divide = (float)tiles < kWholeTiles * (float)workers && workers > 1;
-  if (t == 0) {
-    plan.info[0] = divide ? workers : tiles;
-    plan.info[1] = divide;
-    plan.info[2] = total;
-  }
-  if (!divide) return;
-  __threadfence_block();
-  __syncthreads();
-  for (int64_t w = t; w < workers; w += 1024) {
-    const int64_t x = w * total / workers;
-    int lo = 0, hi = tiles - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (plan.unit_end[mid] > x)
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
-    plan.run_tile[w] = lo;
-  }
-}
 
 // Two transpose reads -> the 8 keys of one element of an A operand: in each
 // group of 16 lanes, lane i receives element i % 4 of the 8-byte reads of
@@ -474,96 +376,16 @@ __global__ __launch_bounds__(64 * W, chunk_wgs_per_cu(D, W) * W / 4) void k_attn
   }
 }
 
-// Joins the parts of the divided tiles: a workgroup per cut, key/value head
-// and 4 rows takes the tile if the cut is the first in it; its waves take
-// parts in turn (a long context has one for every workgroup), a lane D / 64
-// elements of each row.
-constexpr int kJoinRows = 4;
-
-template <int D>
-__global__ __launch_bounds__(256) void k_attn_chunk_join(AttnParams p, ChunkPlan plan) {
-  constexpr int kE = D / 64;
-  __shared__ float s_o[4][kJoinRows][D];
-  __shared__ float s_m[4][kJoinRows], s_l[4][kJoinRows];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int kvh = blockIdx.y;
-  const int64_t w = blockIdx.x + 1, runs = plan.info[0], total = plan.info[2];
-  if (plan.info[1] == 0 || w >= runs) return;
-  const int tile = plan.run_tile[w];
-  const int2 bq = plan.tile[tile];
-  const int64_t end = plan.unit_end[tile], start = tile ? plan.unit_end[tile - 1] : 0;
-  const int64_t cut = w * total / runs, before = (w - 1) * total / runs;
-  if (cut == start || before > start) return;
-  const int64_t first = 2 * (w - 1) + (before != start);
-  const int count = (int)((end * runs - 1) / total - (w - 1)) + 1;
-  const Seq s = load_seq(p, bq.x);
-  const int64_t r0 = (int64_t)bq.y * plan.tile_rows + blockIdx.z * kJoinRows, rows = (int64_t)s.n * p.g;
-  if (r0 < 0 || r0 >= rows) return;
-  auto at = [&](int i) {  // row r0 of part i
-    return ((i == 0 ? first : 2 * (w - 1 + i)) * p.c.H + kvh) * plan.tile_rows + blockIdx.z * kJoinRows;
-  };
-  float m[kJoinRows], l[kJoinRows], o[kJoinRows][kE];
-#pragma unroll
-  for (int k = 0; k < kJoinRows; ++k) {
-    m[k] = -INFINITY, l[k] = 0.0f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) o[k][e] = 0.0f;
-  }
-#pragma unroll 2
-  for (int i = wave; i < count; i += 4)
-#pragma unroll
-    for (int k = 0; k < kJoinRows; ++k) {
-      const float2 ml = plan.part_ml[at(i) + k];
-      const float top = fmaxf(m[k], ml.x), ref = top == -INFINITY ? 0.0f : top;
-      const float keep = __builtin_amdgcn_exp2f(m[k] - ref), f = __builtin_amdgcn_exp2f(ml.x - ref);
-      m[k] = top;
-      l[k] = l[k] * keep + ml.y * f;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) o[k][e] = o[k][e] * keep + plan.part_o[(at(i) + k) * D + kE * lane + e] * f;
-    }
-#pragma unroll
-  for (int k = 0; k < kJoinRows; ++k) {
-    if (lane == 0) s_m[wave][k] = m[k], s_l[wave][k] = l[k];
-#pragma unroll
-    for (int e = 0; e < kE; ++e) s_o[wave][k][kE * lane + e] = o[k][e];
-  }
-  __syncthreads();
-  const int k = wave;  // a row per wave
-  const int64_t r = r0 + k;
-  if (r >= rows) return;
-  const float top = fmaxf(fmaxf(s_m[0][k], s_m[1][k]), fmaxf(s_m[2][k], s_m[3][k]));
-  const float ref = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f, x[kE];
-#pragma unroll
-  for (int e = 0; e < kE; ++e) x[e] = 0.0f;
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const float f = __builtin_amdgcn_exp2f(s_m[v][k] - ref);
-    sum += s_l[v][k] * f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) x[e] += s_o[v][k][kE * lane + e] * f;
-  }
-  const int qi = (int)(r / p.g), qh = kvh * p.g + (int)(r % p.g);
-  const float inv = sum == 0.0f ? 0.0f : *p.c.v_st / sum;
-  uint16_t* out = p.out + (s.row0 + qi) * p.out_ld_t + qh * p.out_ld_h + kE * lane;
-#pragma unroll
-  for (int e = 0; e < kE; ++e) out[e] = (uint16_t)f32_to_bf16_any(x[e] * inv);
-  if (p.lse && lane == 0)
-    p.lse[(int64_t)(s.row0 + qi) * p.Hq + qh] = sum == 0.0f ? -INFINITY : (top + __builtin_log2f(sum)) * kLn2;
-}
-
 template <int D, int W>
 int launch_chunk(const AttnParams& p, const ChunkPlan& plan, hipStream_t s) {
-  hipLaunchKernelGGL(k_attn_chunk_plan, dim3(1), dim3(1024), 0, s, p, plan);
-  if (int rc = last_launch()) return rc;
   const int64_t runs = std::max<int64_t>(plan.max_tiles, plan.workers);
   hipLaunchKernelGGL((k_attn_chunk<D, W>), dim3((unsigned)(runs * p.c.H + plan.check)), dim3(64 * W), 0, s, p, plan);
-  if (int rc = last_launch()) return rc;
-  if (plan.workers == 1) return NVQ_OK;
-  hipLaunchKernelGGL((k_attn_chunk_join<D>),
-                     dim3((unsigned)plan.workers - 1, (unsigned)p.c.H, (unsigned)(plan.tile_rows / kJoinRows)), dim3(256),
-                     0, s, p, plan);
   return last_launch();
+}
+
+__global__ __launch_bounds__(1024) void k_attn_chunk_plan(AttnParams p, ChunkPlan plan) {
+  __shared__ PlanLds lds;
+  plan_chunks(p, plan, lds);
 }
 
 }  // namespace
@@ -577,7 +399,7 @@ void attn_chunk_plan(const AttnParams& p, int min_rows, bool check, WsCarve& ws,
   plan.max_tiles = (int64_t)p.total_q * p.g / plan.tile_rows + p.B;
   const int64_t units = (p.num_keys + kTileKeys - 1) / kTileKeys + 1;  // most of a tile
   const int64_t places = (int64_t)chunk_wgs_per_cu(p.c.D, waves) * device_cu_count() - plan.check;
-  plan.workers = (int)std::max<int64_t>(1, std::min(places / p.c.H, units * plan.max_tiles / kMinUnits));
+  plan.workers = (int)std::max<int64_t>(1, std::min(places / p.c.H, units * plan.max_tiles / kChunkMinUnits));
   plan.info = ws.take<int64_t>(3);
   plan.tile_end = ws.take<int32_t>((size_t)p.B);
   plan.tile = ws.take<int2>((size_t)plan.max_tiles);
@@ -588,7 +410,11 @@ void attn_chunk_plan(const AttnParams& p, int min_rows, bool check, WsCarve& ws,
   plan.part_o = ws.take<float>(rows * p.c.D);
 }
 
-int attn_chunk_launch(const AttnParams& p, const ChunkPlan& plan, hipStream_t s) {
+int attn_chunk_launch(const AttnParams& p, const ChunkPlan& plan, bool planned, hipStream_t s) {
+  if (!planned) {
+    hipLaunchKernelGGL(k_attn_chunk_plan, dim3(1), dim3(1024), 0, s, p, plan);
+    if (int rc = last_launch()) return rc;
+  }
   switch (p.c.D * 16 + plan.tile_rows / 32) {
     case 64 * 16 + 4: return launch_chunk<64, 4>(p, plan, s);
     case 128 * 16 + 4: return launch_chunk<128, 4>(p, plan, s);

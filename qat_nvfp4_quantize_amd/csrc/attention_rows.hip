@@ -35,6 +35,7 @@
 
 #include "nvq.h"
 #include "nvq_attn.h"
+#include "nvq_attn_plan.h"
 #include "nvq_dequant.h"
 #include "nvq_device.h"
 #include "nvq_internal.h"
@@ -166,18 +167,26 @@ __device__ __forceinline__ half2_t scale_two(uint32_t four, int i) {
 }
 
 template <int D, int MT>
-__global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnParams p, RowsPlan plan) {
+__global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnParams p, RowsPlan plan, ChunkPlan chunks) {
   constexpr int kRows = 16 * MT, kTiles = D / 16, kSteps = D / 32;
   constexpr int kPitch = D + 4;  // floats; 16-byte rows shifted over the banks
   __shared__ float s_o[2][kRows * kPitch];
   __shared__ float s_m[4][kRows], s_l[4][kRows];
-  __shared__ CheckLds s_check;
+  __shared__ union {
+    CheckLds check;
+    PlanLds plan;
+  } s_one;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (blockIdx.x == 0) {  // one workgroup more than workers
-    check_batch(p, s_check);
+  // one workgroup more than workers, and one that plans the many-rows launch
+  if (blockIdx.x == 0) {
+    check_batch(p, s_one.check);
     return;
   }
-  const int block = blockIdx.x - 1, kvh = block % p.c.H, worker = block / p.c.H;
+  if (plan.plans_chunks && blockIdx.x == 1) {
+    plan_chunks(p, chunks, s_one.plan);
+    return;
+  }
+  const int block = blockIdx.x - 1 - plan.plans_chunks, kvh = block % p.c.H, worker = block / p.c.H;
 
   // this worker's run [x, x_end) of the units of all sequences
   int chunk = 0, incl = chunk_units(p, plan.max_rows, 0), total = __builtin_amdgcn_readlane(incl, 63);
@@ -460,65 +469,10 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
   }
 }
 
-// Joins the parts of a split sequence: a workgroup per row and key/value
-// head, its four waves taking parts in turn, a lane D / 64 elements.
-template <int D, int kRows>
-__global__ __launch_bounds__(256) void k_attn_rows_join(AttnParams p, RowsPlan plan) {
-  constexpr int kE = D / 64;
-  __shared__ float s_o[4][D];
-  __shared__ float s_l[4], s_m[4];
-  const int b = blockIdx.x, kvh = blockIdx.y, r = blockIdx.z;
-  const Seq s = load_seq(p, b);
-  if (r >= s.n * p.g || s.n * p.g > plan.max_rows) return;
-  const int first = plan.seq[2 * b], count = plan.seq[2 * b + 1];
-  if (count == 1) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  // the first worker's slot as noted, slot 0 of the others
-  auto slot = [&](int i) {
-    return ((int64_t)(i == 0 ? first : 2 * ((first >> 1) + i)) * p.c.H + kvh) * kRows + r;
-  };
-  float m = -INFINITY;
-  for (int i = threadIdx.x; i < count; i += 256) m = fmaxf(m, plan.part_ml[slot(i)].x);
-#pragma unroll
-  for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x, 64));
-  if (lane == 0) s_m[wave] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  const float ref = m == -INFINITY ? 0.0f : m;
-  float o[kE], l = 0.0f;
-#pragma unroll
-  for (int e = 0; e < kE; ++e) o[e] = 0.0f;
-#pragma unroll 8
-  for (int i = wave; i < count; i += 4) {
-    const int64_t at = slot(i);
-    const float2 ml = plan.part_ml[at];
-    const float f = __builtin_amdgcn_exp2f(ml.x - ref);
-    l += ml.y * f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] += plan.part_o[at * D + kE * lane + e] * f;
-  }
-#pragma unroll
-  for (int e = 0; e < kE; ++e) s_o[wave][kE * lane + e] = o[e];
-  if (lane == 0) s_l[wave] = l;
-  __syncthreads();
-  const float sum = s_l[0] + s_l[1] + s_l[2] + s_l[3];
-  const int i = r / p.g, h = kvh * p.g + (r - i * p.g);
-  const float inv = sum == 0.0f ? 0.0f : *p.c.v_st / sum;
-  for (int d = threadIdx.x; d < D; d += 256)
-    p.out[(s.row0 + i) * p.out_ld_t + h * p.out_ld_h + d] =
-        (uint16_t)f32_to_bf16_any((s_o[0][d] + s_o[1][d] + s_o[2][d] + s_o[3][d]) * inv);
-  if (p.lse && threadIdx.x == 0)
-    p.lse[(int64_t)(s.row0 + i) * p.Hq + h] = sum == 0.0f ? -INFINITY : (m + __builtin_log2f(sum)) * kLn2;
-}
-
 template <int D, int MT>
-int launch_rows(const AttnParams& p, const RowsPlan& plan, hipStream_t s) {
-  hipLaunchKernelGGL((k_attn_rows<D, MT>), dim3((unsigned)(plan.workers * p.c.H + 1)), dim3(256), 0, s, p, plan);
-  if (int rc = last_launch()) return rc;
-  if (!plan.may_split) return NVQ_OK;
-  const int rows = std::min<int64_t>((int64_t)p.max_q * p.g, 16 * MT);
-  hipLaunchKernelGGL((k_attn_rows_join<D, 16 * MT>), dim3((unsigned)p.B, (unsigned)p.c.H, (unsigned)rows), dim3(256),
-                     0, s, p, plan);
+int launch_rows(const AttnParams& p, const RowsPlan& plan, const ChunkPlan& chunk, hipStream_t s) {
+  hipLaunchKernelGGL((k_attn_rows<D, MT>), dim3((unsigned)(plan.workers * p.c.H + 1 + plan.plans_chunks)), dim3(256), 0,
+                     s, p, plan, chunk);
   return last_launch();
 }
 
@@ -530,11 +484,12 @@ int attn_rows_tiles(int D, int64_t rows) {
   return rows <= (D == 256 ? 32 : 64) ? (int)((rows + 15) / 16) : 0;
 }
 
-void attn_rows_plan(const AttnParams& p, int tiles, WsCarve& ws, RowsPlan& plan) {
+void attn_rows_plan(const AttnParams& p, int tiles, bool chunks, WsCarve& ws, RowsPlan& plan) {
+  plan.plans_chunks = chunks;
   plan.max_rows = 16 * tiles;
   const int64_t units = (p.num_keys + kUnit - 1) / kUnit + 1;  // most of a sequence
   const int64_t places = (int64_t)rows_wgs_per_cu(p.c.D, tiles) * device_cu_count();
-  plan.workers = (int)std::max<int64_t>(1, std::min((places - 1) / p.c.H, units * p.B / kMinUnits));
+  plan.workers = (int)std::max<int64_t>(1, std::min((places - 1 - chunks) / p.c.H, units * p.B / kMinUnits));
   plan.may_split = plan.workers > 1;
   plan.seq = ws.take<int32_t>(2 * (size_t)p.B);
   const size_t rows = plan.may_split ? (size_t)(2 * plan.workers * p.c.H) * plan.max_rows : 0;
@@ -542,18 +497,18 @@ void attn_rows_plan(const AttnParams& p, int tiles, WsCarve& ws, RowsPlan& plan)
   plan.part_o = ws.take<float>(rows * p.c.D);
 }
 
-int attn_rows_launch(const AttnParams& p, const RowsPlan& plan, hipStream_t s) {
+int attn_rows_launch(const AttnParams& p, const RowsPlan& plan, const ChunkPlan& chunk, hipStream_t s) {
   switch (p.c.D * 8 + plan.max_rows / 16) {
-    case 64 * 8 + 1: return launch_rows<64, 1>(p, plan, s);
-    case 64 * 8 + 2: return launch_rows<64, 2>(p, plan, s);
-    case 64 * 8 + 3: return launch_rows<64, 3>(p, plan, s);
-    case 64 * 8 + 4: return launch_rows<64, 4>(p, plan, s);
-    case 128 * 8 + 1: return launch_rows<128, 1>(p, plan, s);
-    case 128 * 8 + 2: return launch_rows<128, 2>(p, plan, s);
-    case 128 * 8 + 3: return launch_rows<128, 3>(p, plan, s);
-    case 128 * 8 + 4: return launch_rows<128, 4>(p, plan, s);
-    case 256 * 8 + 1: return launch_rows<256, 1>(p, plan, s);
-    default: return launch_rows<256, 2>(p, plan, s);
+    case 64 * 8 + 1: return launch_rows<64, 1>(p, plan, chunk, s);
+    case 64 * 8 + 2: return launch_rows<64, 2>(p, plan, chunk, s);
+    case 64 * 8 + 3: return launch_rows<64, 3>(p, plan, chunk, s);
+    case 64 * 8 + 4: return launch_rows<64, 4>(p, plan, chunk, s);
+    case 128 * 8 + 1: return launch_rows<128, 1>(p, plan, chunk, s);
+    case 128 * 8 + 2: return launch_rows<128, 2>(p, plan, chunk, s);
+    case 128 * 8 + 3: return launch_rows<128, 3>(p, plan, chunk, s);
+    case 128 * 8 + 4: return launch_rows<128, 4>(p, plan, chunk, s);
+    case 256 * 8 + 1: return launch_rows<256, 1>(p, plan, chunk, s);
+    default: return launch_rows<256, 2>(p, plan, chunk, s);
   }
 }
 

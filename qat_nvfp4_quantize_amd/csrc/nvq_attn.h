@@ -31,14 +31,14 @@ struct RowsPlan {
   int max_rows;  // sequences with more rows per key/value head are left out
   int workers;   // most workgroups per key/value head
   int may_split;
+  int plans_chunks;  // the launch has a workgroup that plans the many-rows one
   int32_t* seq;     // [B][2]: first worker and its slot (2 worker + slot), number of workers
   float2* part_ml;  // [worker][2 slots][head][max_rows] reference and sum
   float* part_o;    // [worker][2 slots][head][max_rows][D]
 };
 
 int attn_rows_tiles(int D, int64_t rows);
-void attn_rows_plan(const AttnParams& p, int tiles, WsCarve& ws, RowsPlan& plan);
-int attn_rows_launch(const AttnParams& p, const RowsPlan& plan, hipStream_t s);
+void attn_rows_plan(const AttnParams& p, int tiles, bool chunks, WsCarve& ws, RowsPlan& plan);
 
 // Plan of the many-rows kernel: row tiles and their key tiles in one
 // row of units per key/value head, cut into runs, and where the parts of tiles
@@ -59,7 +59,10 @@ struct ChunkPlan {
 };
 
 void attn_chunk_plan(const AttnParams& p, int min_rows, bool check, WsCarve& ws, ChunkPlan& plan);
-int attn_chunk_launch(const AttnParams& p, const ChunkPlan& plan, hipStream_t s);
+int attn_chunk_launch(const AttnParams& p, const ChunkPlan& plan, bool planned, hipStream_t s);
+int attn_rows_launch(const AttnParams& p, const RowsPlan& plan, const ChunkPlan& chunk, hipStream_t s);
+// Joins what either kernel left in parts (a NULL plan: that kernel did not run).
+int attn_join_launch(const AttnParams& p, const RowsPlan* rows, const ChunkPlan* chunk, hipStream_t s);
 
 constexpr float kLn2 = 0.69314718055994530942f;
 

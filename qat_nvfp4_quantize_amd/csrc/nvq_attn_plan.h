@@ -1,0 +1,116 @@
+// Row tiles of the many-rows attention kernel and the plan of a call: used by
+// the workgroup that plans, which rides on the few-rows launch where a batch
+// has one, and by the kernel itself.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "nvq_attn.h"
+#include "nvq_scan.h"
+
+namespace nvq {
+
+constexpr int kTileKeys = 64;
+constexpr int kChunkMinUnits = 4;  // key tiles of a run, where there are so many
+// With this many row tiles per place they go out whole, the ones with most
+// keys first; with fewer the units are dealt in equal runs, which costs a
+// second pass over the divided tiles.
+constexpr float kWholeTiles = 1.5f;
+
+
+// Keys of row tile qt of sequence s, in 64-key tiles from `base`.
+struct TileRange {
+  int64_t base, hi;
+  int units;
+};
+__device__ __forceinline__ TileRange tile_range(const AttnParams& p, const Seq& s, int qt, int tile_rows) {
+  const int i0 = (int)((int64_t)qt * tile_rows / p.g);
+  const int i1 = min(s.n - 1, (int)(((int64_t)(qt + 1) * tile_rows - 1) / p.g));
+  TileRange r;
+  int64_t lo, x;
+  visible(p, s, s.pos0 + i0, lo, x);
+  visible(p, s, s.pos0 + i1, x, r.hi);
+  r.base = lo & ~(int64_t)(kTileKeys - 1);
+  r.units = r.hi > r.base ? (int)((r.hi - r.base + kTileKeys - 1) / kTileKeys) : 1;
+  return r;
+}
+
+struct PlanLds {
+  int end[1024];  // tile_end of the first 1024 sequences
+  int scan[16];
+  int last;
+};
+
+// One workgroup (256 or 1024 threads) plans the call: the row tiles of the sequences (the last rows,
+// which see the most keys, first), the units up to each, and the cuts.
+__device__ __forceinline__ void plan_chunks(const AttnParams& p, const ChunkPlan& plan, PlanLds& lds) {
+  const int t = threadIdx.x, threads = blockDim.x;
+  auto last = [&](int incl) {  // the workgroup's total of an inclusive scan
+    __syncthreads();
+    if (t == threads - 1) lds.last = incl;
+    __syncthreads();
+    return lds.last;
+  };
+  int tiles = 0;
+  for (int b0 = 0; b0 < p.B; b0 += threads) {
+    int n = 0;
+    if (b0 + t < p.B) {
+      const Seq s = load_seq(p, b0 + t);
+      const int64_t rows = (int64_t)s.n * p.g;
+      n = rows > plan.min_rows ? (int)((rows + plan.tile_rows - 1) / plan.tile_rows) : 0;
+    }
+    const int incl = block_inclusive_scan(n, lds.scan);
+    if (b0 + t < 1024) lds.end[b0 + t] = tiles + incl;
+    if (b0 + t < p.B) plan.tile_end[b0 + t] = tiles + incl;
+    tiles += last(incl);
+  }
+  tiles = (int)min<int64_t>(tiles, plan.max_tiles);  // overlapping row ranges could name more
+  __threadfence_block();
+  __syncthreads();
+  auto end_of = [&](int b) { return b < 1024 ? lds.end[b] : plan.tile_end[b]; };
+  int64_t total = 0;
+  for (int i0 = 0; i0 < tiles; i0 += threads) {
+    const int i = i0 + t;
+    int units = 0;
+    if (i < tiles) {
+      int lo = 0, hi = p.B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (end_of(mid) > i)
+          hi = mid;
+        else
+          lo = mid + 1;
+      }
+      const int qt = end_of(lo) - 1 - i;
+      units = tile_range(p, load_seq(p, lo), qt, plan.tile_rows).units;
+      plan.tile[i] = make_int2(lo, qt);
+    }
+    const int incl = block_inclusive_scan(units, lds.scan);
+    if (i < tiles) plan.unit_end[i] = total + incl;
+    total += last(incl);
+  }
+  const int64_t workers = max<int64_t>(1, min<int64_t>(plan.workers, total / kChunkMinUnits));
+  const bool divide = (float)tiles < kWholeTiles * (float)workers && workers > 1;
+  if (t == 0) {
+    plan.info[0] = divide ? workers : tiles;
+    plan.info[1] = divide;
+    plan.info[2] = total;
+  }
+  if (!divide) return;
+  __threadfence_block();
+  __syncthreads();
+  for (int64_t w = t; w < workers; w += threads) {
+    const int64_t x = w * total / workers;
+    int lo = 0, hi = tiles - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (plan.unit_end[mid] > x)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    plan.run_tile[w] = lo;
+  }
+}
+
+}  // namespace nvq
