@@ -1,11 +1,14 @@
 // Paged NVFP4 KV cache: new K and V tokens quantized as they are written into
 // their slots, and slots read back.
 //
-// Both kernels are HBM-bound (2 or 4 bytes a value against 0.5625), one
-// 16-element block per thread.  A workgroup takes consecutive tokens of one
-// head: where a sequence's tokens fill a page in order, the page's 64-byte
-// code rows and the V scales (slots innermost) of those tokens are written by
-// one workgroup, so one L2 merges them into whole lines.
+// Both kernels are HBM-bound (2 or 4 bytes a value against 0.5625).  A workgroup takes consecutive tokens of one
+// head, and workgroups are numbered heads first: they go to the eight XCDs in
+// turn, so with 8 heads (or 4) an XCD sees one head (or half of its tokens).
+// A token's V scales are single bytes in lines that the head's other slots
+// share; kept to one L2 they are merged there.  32768 tokens of 8 heads x 128
+// bf16 (172 MB at the least): 36 us with whole pages in order (4.8 TB/s), 54
+// with slots in random order, against 45 and 62 with workgroups numbered
+// tokens first.
 //
 // This translation unit is compiled with -ffp-contract=off (nvq_quant_block.h).
 
@@ -24,28 +27,38 @@ namespace {
 
 constexpr int kKvThreads = 256;
 
+// Token groups over y and z (y alone stops at 65535).
+constexpr int kGroupsY = 32768;
+__device__ __forceinline__ int64_t token_group() { return (int64_t)blockIdx.z * gridDim.y + blockIdx.y; }
+dim3 kv_grid(const KvPages& c, int64_t T, int rows, int parts) {
+  const int64_t groups = (T + rows - 1) / rows, y = std::min<int64_t>(groups, kGroupsY);
+  return dim3((unsigned)(parts * c.H), (unsigned)y, (unsigned)((groups + y - 1) / y));
+}
+
 struct KvAppendParams {
   KvPages c;
   const char* src[2];        // k, v
   int64_t ld_t[2], ld_h[2];  // bytes
   const int32_t* slots;
   int64_t T;
-  int rows;  // tokens of a workgroup: kKvThreads / (D / 16), at least 1
+  int rows;  // tokens of a workgroup's step: kKvThreads / (D / 16)
   uint32_t* status;
 };
 
-// blockIdx: x token group, y head, z 0 for K and 1 for V.
+// Grid: x = head (K) or H + head (V), y and z the token group.  One block a
+// thread (4 tokens a thread, loaded ahead, measured 59 us against 54).
 template <bool kBF16>
 __global__ __launch_bounds__(kKvThreads) void k_kv_append(KvAppendParams p) {
   __shared__ uint32_t s_slot[kKvThreads * (kBF16 ? 8 : 16)];
-  const int nb = p.c.D >> 4, h = blockIdx.y;
+  const int nb = p.c.D >> 4;
+  const bool is_v = (int)blockIdx.x >= p.c.H;
+  const int h = blockIdx.x - (is_v ? p.c.H : 0);
   const int r = threadIdx.x / nb, blk = threadIdx.x - r * nb;
-  const int64_t t = (int64_t)blockIdx.x * p.rows + r;
+  const int64_t t = token_group() * p.rows + r;
   uint32_t bad = 0;
   if (r < p.rows && t < p.T) {
     const int32_t slot = p.slots[t];
     if (slot >= 0 && slot < p.c.num_slots) {
-      const bool is_v = blockIdx.z != 0;
       RowBlock<kBF16> rb;
       rb.load_at(p.src[is_v] + t * p.ld_t[is_v] + h * p.ld_h[is_v] + blk * (kBF16 ? 32 : 64));
       const float s_t = *(is_v ? p.c.v_st : p.c.k_st);
@@ -60,15 +73,14 @@ __global__ __launch_bounds__(kKvThreads) void k_kv_append(KvAppendParams p) {
                                         nonfinite, lds);
       else
         encode_block_exact<kBF16, false>(rb, s_t, six_st, sc, cw, acc, nonfinite, lds);
-      const int64_t page = slot >> p.c.log_ps;
+      if (nonfinite) bad |= (uint32_t)NVQ_STATUS_NONFINITE;
       const int off = slot & (p.c.ps - 1);
-      const int64_t tile = (page * p.c.H + h) << p.c.log_ps;  // first slot row of (page, head)
+      const int64_t tile = ((int64_t)(slot >> p.c.log_ps) * p.c.H + h) << p.c.log_ps;  // first row of (page, head)
       *reinterpret_cast<uint2*>((is_v ? p.c.v_codes : p.c.k_codes) + ((tile + off) * nb + blk) * 8) = cw;
       if (is_v)
         p.c.v_scales[tile * nb + ((int64_t)blk << p.c.log_ps) + off] = (uint8_t)sc;
       else
         p.c.k_scales[(tile + off) * nb + blk] = (uint8_t)sc;
-      if (nonfinite) bad |= (uint32_t)NVQ_STATUS_NONFINITE;
     } else if (slot >= 0) {
       bad |= (uint32_t)NVQ_STATUS_BAD_SLOT;
     }
@@ -82,40 +94,74 @@ struct KvGatherParams {
   char* dst[2];  // k_out, v_out; NULL: not wanted
   const int32_t* slots;
   int64_t T;
-  int rows;
+  int rows;  // tokens of a workgroup's step
   int z0;  // first of the wanted outputs
   uint32_t* status;
 };
 
-template <bool kBF16>
+// A thread writes 16 bytes (8 bf16 or 4 fp32 values) of kTok tokens, so a
+// wave's stores are whole lines.
+template <bool kBF16, int kTok>
 __global__ __launch_bounds__(kKvThreads) void k_kv_gather(KvGatherParams p) {
-  const int nb = p.c.D >> 4, h = blockIdx.y;
-  const int r = threadIdx.x / nb, blk = threadIdx.x - r * nb;
-  const int64_t t = (int64_t)blockIdx.x * p.rows + r;
+  constexpr int kN = kBF16 ? 8 : 4;
+  const int vecs = p.c.D / kN, nb = p.c.D >> 4;
+  const bool second = (int)blockIdx.x >= p.c.H, is_v = second || p.z0;
+  const int h = blockIdx.x - (second ? p.c.H : 0);
+  const int r = threadIdx.x / vecs, vec = threadIdx.x - r * vecs, blk = vec * kN / 16;
+  const int64_t t0 = token_group() * (kTok * p.rows) + r;
   uint32_t bad = 0;
-  if (r < p.rows && t < p.T) {
-    const bool is_v = p.z0 + (int)blockIdx.z != 0;
-    const int32_t slot = p.slots[t];
-    uint2 cw = make_uint2(0u, 0u);
-    float s_b = 0.0f;
-    if (slot >= 0 && slot < p.c.num_slots) {
-      const int64_t page = slot >> p.c.log_ps;
-      const int off = slot & (p.c.ps - 1);
-      const int64_t tile = (page * p.c.H + h) << p.c.log_ps;
-      cw = *reinterpret_cast<const uint2*>((is_v ? p.c.v_codes : p.c.k_codes) + ((tile + off) * nb + blk) * 8);
-      s_b = e4m3_to_f32(is_v ? p.c.v_scales[tile * nb + ((int64_t)blk << p.c.log_ps) + off]
-                             : p.c.k_scales[(tile + off) * nb + blk]);
-    } else if (slot >= 0) {
-      bad = (uint32_t)NVQ_STATUS_BAD_SLOT;
+  if (r < p.rows) {
+    int32_t slot[kTok];
+    uint32_t w[kTok], sc[kTok];
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      const int64_t t = t0 + i * p.rows;
+      slot[i] = t < p.T ? p.slots[t] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      w[i] = sc[i] = 0u;
+      if (slot[i] >= 0 && slot[i] < p.c.num_slots) {
+        const int off = slot[i] & (p.c.ps - 1);
+        const int64_t tile = ((int64_t)(slot[i] >> p.c.log_ps) * p.c.H + h) << p.c.log_ps;
+        const uint8_t* at = (is_v ? p.c.v_codes : p.c.k_codes) + (tile + off) * (p.c.D >> 1) + vec * (kN / 2);
+        w[i] = kBF16 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
+        sc[i] = is_v ? p.c.v_scales[tile * nb + ((int64_t)blk << p.c.log_ps) + off] : p.c.k_scales[(tile + off) * nb + blk];
+      } else if (slot[i] >= 0) {
+        bad = (uint32_t)NVQ_STATUS_BAD_SLOT;
+      }
     }
     const float s_t = *(is_v ? p.c.v_st : p.c.k_st);
-    float v[16];
-    block_values(cw, s_b, s_t, v);
-    char* out = p.dst[is_v] + ((t * p.c.H + h) * nb + blk) * (kBF16 ? 32 : 64);
-    store_block<kBF16>(v, out);
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      const int64_t t = t0 + i * p.rows;
+      if (t >= p.T) break;
+      const float s_b = e4m3_to_f32(sc[i]);
+      const float2 a = fp4_pair_to_f32<0>(w[i]), b = fp4_pair_to_f32<1>(w[i]);
+      uint4 out;
+      if constexpr (kBF16) {
+        const float2 c = fp4_pair_to_f32<2>(w[i]), d = fp4_pair_to_f32<3>(w[i]);
+        auto two = [&](float2 g) {
+          return f32_to_bf16_rne((g.x * s_b) * s_t) | (f32_to_bf16_rne((g.y * s_b) * s_t) << 16);
+        };
+        out = make_uint4(two(a), two(b), two(c), two(d));
+      } else {
+        auto one = [&](float g) { return __float_as_uint((g * s_b) * s_t); };
+        out = make_uint4(one(a.x), one(a.y), one(b.x), one(b.y));
+      }
+      *reinterpret_cast<uint4*>(p.dst[is_v] + (((t * p.c.H + h) * vecs) + vec) * 16) = out;
+    }
   }
   bad = wave_or_u32(bad);
   if (bad && p.status && (threadIdx.x & 63) == 0) atomicOr(p.status, bad);
+}
+
+// Four tokens a thread where that leaves every CU a few workgroups (32768
+// tokens in page order: 41 us against 49 with one; in random order 56 and 62,
+// most of it lines read for 64 of their 128 bytes and for single V scales).
+constexpr int kManyTokens = 4;
+bool many_tokens(const KvPages& c, int64_t T, int rows) {
+  return 2 * c.H * (T / (kManyTokens * rows)) >= 4 * (int64_t)device_cu_count();
 }
 
 int check_ws(void* ws, size_t ws_bytes) {
@@ -155,7 +201,7 @@ extern "C" int nvq_kv_append(const nvq_kv_cache* cache, const void* k, const voi
   p.slots = slots, p.T = T;
   p.rows = kKvThreads / (p.c.D / 16);
   p.status = static_cast<uint32_t*>(ws);
-  const dim3 grid((unsigned)((T + p.rows - 1) / p.rows), (unsigned)p.c.H, 2);
+  const dim3 grid = kv_grid(p.c, T, p.rows, 2);
   if (dtype == NVQ_BF16)
     hipLaunchKernelGGL(k_kv_append<true>, grid, dim3(kKvThreads), 0, s, p);
   else
@@ -178,13 +224,19 @@ extern "C" int nvq_kv_gather(const nvq_kv_cache* cache, const int32_t* slots, in
   if (T == 0) return NVQ_OK;
   p.dst[0] = static_cast<char*>(k_out), p.dst[1] = static_cast<char*>(v_out);
   p.slots = slots, p.T = T;
-  p.rows = kKvThreads / (p.c.D / 16);
+  const bool bf16 = out_dtype == NVQ_BF16;
+  p.rows = kKvThreads / (p.c.D / (bf16 ? 8 : 4));
   p.z0 = k_out ? 0 : 1;
   p.status = static_cast<uint32_t*>(ws);
-  const dim3 grid((unsigned)((T + p.rows - 1) / p.rows), (unsigned)p.c.H, (k_out && v_out) ? 2 : 1);
-  if (out_dtype == NVQ_BF16)
-    hipLaunchKernelGGL(k_kv_gather<true>, grid, dim3(kKvThreads), 0, s, p);
+  const bool many = many_tokens(p.c, T, p.rows);
+  const dim3 grid = kv_grid(p.c, T, p.rows * (many ? kManyTokens : 1), k_out && v_out ? 2 : 1);
+  if (bf16 && many)
+    hipLaunchKernelGGL((k_kv_gather<true, kManyTokens>), grid, dim3(kKvThreads), 0, s, p);
+  else if (bf16)
+    hipLaunchKernelGGL((k_kv_gather<true, 1>), grid, dim3(kKvThreads), 0, s, p);
+  else if (many)
+    hipLaunchKernelGGL((k_kv_gather<false, kManyTokens>), grid, dim3(kKvThreads), 0, s, p);
   else
-    hipLaunchKernelGGL(k_kv_gather<false>, grid, dim3(kKvThreads), 0, s, p);
+    hipLaunchKernelGGL((k_kv_gather<false, 1>), grid, dim3(kKvThreads), 0, s, p);
   return last_launch();
 }

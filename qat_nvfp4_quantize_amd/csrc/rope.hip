@@ -12,6 +12,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "nvq.h"
 #include "nvq_device.h"
@@ -40,8 +41,7 @@ template <bool kBF16>
 struct RopeVec {
   static constexpr int kN = kBF16 ? 8 : 4;
   float v[kN];
-  __device__ __forceinline__ void load(const char* at) {
-    const uint4 q = *reinterpret_cast<const uint4*>(at);
+  __device__ __forceinline__ void unpack(uint4 q) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -63,10 +63,10 @@ struct RopeVec {
   }
 };
 
-// kVec: 16-byte vectors of a row's elements, else single pairs (any size,
-// stride and element alignment).  Items of a row: its rotated vectors (half
-// layout: a vector of each half; interleaved: a vector of whole pairs), then
-// the copied rest.  HBM-bound: every element is read and written once.
+// kVec: 16-byte vectors of a row's elements (half layout: a vector of each
+// half; interleaved: a vector of whole pairs; then the copied rest), else
+// single pairs (any size, stride and element alignment).  HBM-bound: every
+// element is read and written once.
 template <bool kBF16, bool kInter, bool kVec>
 __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeParams p) {
   extern __shared__ float2 s_cs[];  // [tt][rot / 2] (m cos, +-m sin)
@@ -85,69 +85,91 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeParams p) {
   }
   __syncthreads();
   const int h0 = blockIdx.y * p.hc, hn = min(p.hc, p.H - h0);
-  const int n_rot = (kInter && kVec) ? p.rot / kN : half / kN;
-  const int per_row = n_rot + (p.copy_rest ? (p.D - p.rot) / kN : 0);
-  const int items = tn * hn * per_row;
-  for (int it = threadIdx.x; it < items; it += kRopeThreads) {
-    const int row = it / per_row, c = it - row * per_row;
-    const int tok = row / hn, h = h0 + (row - tok * hn);
-    const int64_t t = t0 + tok;
-    const char* xr = p.x + (t * p.x_ld_t + h * p.x_ld_h) * kSize;
-    char* yr = p.y + (t * p.y_ld_t + h * p.y_ld_h) * kSize;
-    if (c >= n_rot) {
-      const int64_t at = (int64_t)(p.rot + (c - n_rot) * kN) * kSize;
-      if (kVec)
-        *reinterpret_cast<uint4*>(yr + at) = *reinterpret_cast<const uint4*>(xr + at);
-      else if (kBF16)
-        *reinterpret_cast<uint16_t*>(yr + at) = *reinterpret_cast<const uint16_t*>(xr + at);
-      else
-        *reinterpret_cast<uint32_t*>(yr + at) = *reinterpret_cast<const uint32_t*>(xr + at);
-      continue;
-    }
-    const float2* cs = s_cs + tok * half;
-    if constexpr (!kVec) {
+  if constexpr (!kVec) {
+    const int per_row = half + (p.copy_rest ? p.D - p.rot : 0);
+    for (int it = threadIdx.x; it < tn * hn * per_row; it += kRopeThreads) {
+      const int row = it / per_row, c = it - row * per_row, tok = row / hn;
+      const int64_t t = t0 + tok, h = h0 + (row - tok * hn);
+      using Elem = std::conditional_t<kBF16, uint16_t, float>;
+      const Elem* xr = reinterpret_cast<const Elem*>(p.x) + t * p.x_ld_t + h * p.x_ld_h;
+      Elem* yr = reinterpret_cast<Elem*>(p.y) + t * p.y_ld_t + h * p.y_ld_h;
+      if (c >= half) {
+        yr[p.rot + c - half] = xr[p.rot + c - half];
+        continue;
+      }
       const int u = kInter ? 2 * c : c, w = kInter ? 2 * c + 1 : c + half;
-      float a, b;
-      if (kBF16) {
-        a = bf16_to_f32(reinterpret_cast<const uint16_t*>(xr)[u]);
-        b = bf16_to_f32(reinterpret_cast<const uint16_t*>(xr)[w]);
+      const float2 q = s_cs[tok * half + c];
+      if constexpr (kBF16) {
+        const float a = bf16_to_f32(xr[u]), b = bf16_to_f32(xr[w]);
+        yr[u] = (uint16_t)f32_to_bf16_any(a * q.x - b * q.y);
+        yr[w] = (uint16_t)f32_to_bf16_any(a * q.y + b * q.x);
       } else {
-        a = reinterpret_cast<const float*>(xr)[u];
-        b = reinterpret_cast<const float*>(xr)[w];
+        const float a = xr[u], b = xr[w];
+        yr[u] = a * q.x - b * q.y;
+        yr[w] = a * q.y + b * q.x;
       }
-      const float2 q = cs[c];
-      const float ya = a * q.x - b * q.y, yb = a * q.y + b * q.x;
-      if (kBF16) {
-        reinterpret_cast<uint16_t*>(yr)[u] = (uint16_t)f32_to_bf16_any(ya);
-        reinterpret_cast<uint16_t*>(yr)[w] = (uint16_t)f32_to_bf16_any(yb);
-      } else {
-        reinterpret_cast<float*>(yr)[u] = ya;
-        reinterpret_cast<float*>(yr)[w] = yb;
-      }
-    } else if constexpr (kInter) {
-      RopeVec<kBF16> a;
-      a.load(xr + (int64_t)c * 16);
+    }
+  } else {
+    // A thread keeps its vector c of the row (two of them in the half layout)
+    // and walks the rows, kAtOnce of them loaded before the first is stored.
+    constexpr int kAtOnce = kInter ? 4 : 2;
+    const int n_rot = (kInter ? p.rot : half) / kN, per_row = n_rot + (p.copy_rest ? (p.D - p.rot) / kN : 0);
+    const int lanes = min(per_row, kRopeThreads), step = kRopeThreads / lanes;
+    const int first = threadIdx.x / lanes;
+    if (first >= step) return;  // threads past the last whole row
+    for (int c = threadIdx.x - first * lanes; c < per_row; c += lanes) {
+      const bool turn = c < n_rot;
+      const int64_t at = turn ? (int64_t)c * 16 : (int64_t)p.rot * kSize + (int64_t)(c - n_rot) * 16;
+      const int64_t second = (int64_t)half * kSize;
+      int tok = first / hn, h = first - tok * hn;
+      while (tok < tn) {
+        uint4 a[kAtOnce], b[kAtOnce];
+        int rt[kAtOnce], rh[kAtOnce];
 #pragma unroll
-      for (int i = 0; i < kN / 2; ++i) {
-        const float2 q = cs[c * (kN / 2) + i];
-        const float u = a.v[2 * i], w = a.v[2 * i + 1];
-        a.v[2 * i] = u * q.x - w * q.y;
-        a.v[2 * i + 1] = u * q.y + w * q.x;
-      }
-      a.store(yr + (int64_t)c * 16);
-    } else {
-      RopeVec<kBF16> a, b;
-      a.load(xr + (int64_t)c * 16);
-      b.load(xr + (int64_t)half * kSize + (int64_t)c * 16);
+        for (int i = 0; i < kAtOnce; ++i) {
+          rt[i] = tok, rh[i] = h0 + h;
+          if (tok < tn) {
+            const char* xr = p.x + ((t0 + tok) * p.x_ld_t + rh[i] * p.x_ld_h) * kSize + at;
+            a[i] = *reinterpret_cast<const uint4*>(xr);
+            if (!kInter && turn) b[i] = *reinterpret_cast<const uint4*>(xr + second);
+          }
+          h += step;
+          while (h >= hn) h -= hn, ++tok;
+        }
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const float2 q = cs[c * kN + i];
-        const float u = a.v[i], w = b.v[i];
-        a.v[i] = u * q.x - w * q.y;
-        b.v[i] = u * q.y + w * q.x;
+        for (int i = 0; i < kAtOnce; ++i) {
+          if (rt[i] >= tn) break;
+          char* yr = p.y + ((t0 + rt[i]) * p.y_ld_t + rh[i] * p.y_ld_h) * kSize + at;
+          if (!turn) {
+            *reinterpret_cast<uint4*>(yr) = a[i];
+            continue;
+          }
+          const float2* cs = s_cs + rt[i] * half + (kInter ? c * (kN / 2) : c * kN);
+          RopeVec<kBF16> u;
+          u.unpack(a[i]);
+          if constexpr (kInter) {
+#pragma unroll
+            for (int j = 0; j < kN; j += 2) {
+              const float2 q = cs[j / 2];
+              const float m = u.v[j], n = u.v[j + 1];
+              u.v[j] = m * q.x - n * q.y;
+              u.v[j + 1] = m * q.y + n * q.x;
+            }
+          } else {
+            RopeVec<kBF16> w;
+            w.unpack(b[i]);
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+              const float2 q = cs[j];
+              const float m = u.v[j], n = w.v[j];
+              u.v[j] = m * q.x - n * q.y;
+              w.v[j] = m * q.y + n * q.x;
+            }
+            w.store(yr + second);
+          }
+          u.store(yr);
+        }
       }
-      a.store(yr + (int64_t)c * 16);
-      b.store(yr + (int64_t)half * kSize + (int64_t)c * 16);
     }
   }
 }
