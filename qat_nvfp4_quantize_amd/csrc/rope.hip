@@ -224,10 +224,13 @@ extern "C" int nvq_rope(const void* x, int dtype, int64_t T, int64_t H, int64_t 
   const bool inter = layout == NVQ_ROPE_INTERLEAVED;
   const int half = p.rot / 2, step = vec ? n : 1;
   const int64_t per_row = (inter && vec ? p.rot : half) / step + (p.copy_rest ? (p.D - p.rot) / step : 0);
-  // About four items a thread, fewer where that leaves CUs without a workgroup.
+  // Up to 16 vectors a thread, fewer where that leaves CUs without a
+  // workgroup: a workgroup takes the sines of its tokens anew, which at 4
+  // vectors cost as much as the rotation (8192 x 40 x 128 bf16, 64 elements
+  // turned: 44 us against 38; a copy of the tensor 33).
   const int64_t per_wg =
-      std::clamp<int64_t>(T * H * per_row / (4 * (int64_t)device_cu_count()), kRopeThreads, 4 * kRopeThreads);
-  p.tt = (int)std::clamp<int64_t>(2 * kRopeThreads / half, 1, std::min<int64_t>(16, T));
+      std::clamp<int64_t>(T * H * per_row / (4 * (int64_t)device_cu_count()), kRopeThreads, 16 * kRopeThreads);
+  p.tt = (int)std::clamp<int64_t>(kRopeThreads / half, 1, std::min<int64_t>(16, T));
   p.hc = (int)std::clamp<int64_t>(per_wg / (p.tt * per_row), 1, H);
   const int64_t gx = (T + p.tt - 1) / p.tt, gy = (H + p.hc - 1) / p.hc;
   const dim3 grid((unsigned)gx, (unsigned)gy);
