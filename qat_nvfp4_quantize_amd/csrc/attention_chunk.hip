@@ -132,6 +132,34 @@ struct ChunkLds {
   static __device__ __forceinline__ int at(int key) { return (key & 3) * kPlane + (key >> 2) * kRow; }
 };
 
+// o *= keep.  With one wave per SIMD (kInAgprs) the sums live in accumulation
+// registers, and are multiplied there one by one.  Written as a plain product
+// the two ways out of the rare branch met in vector registers, and every tile
+// moved the sums over and back (12 chunks of 700 rows at head dimension 256:
+// 324 -> 299 us).  The s_nops, tied to the sums, are the wait states between
+// the matrix unit's accesses to these registers and those of the vector unit.
+template <bool kInAgprs, int kN>
+__device__ __forceinline__ void rescale(floatx16_t (&o)[kN], float keep) {
+  if constexpr (!kInAgprs) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) o[i] *= keep;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      asm volatile("s_nop 15\n\ts_nop 7" : "+a"(o[i]));
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        float x = o[i][v], t;
+        asm volatile("v_accvgpr_read_b32 %1, %0\n\tv_mul_f32 %1, %1, %2\n\tv_accvgpr_write_b32 %0, %1"
+                     : "+a"(x), "=&v"(t)
+                     : "v"(keep));
+        o[i][v] = x;
+      }
+      asm volatile("s_nop 7" : "+a"(o[i]));
+    }
+  }
+}
+
 // Largest of three (v_max3_f32; fmaxf would first quiet each operand).
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float m;
@@ -314,8 +342,7 @@ __global__ __launch_bounds__(64 * W, chunk_wgs_per_cu(D, W) * W / 4) void k_attn
       ref = moved;
       ref_safe = moved == -INFINITY ? 0.0f : moved;
       l *= keep;
-#pragma unroll
-      for (int i = 0; i < kOut; ++i) o[i] *= keep;
+      rescale<D == 256>(o, keep);
     }
     const NVQ_LDS char* vt = (const NVQ_LDS char*)lds.v[buf] + tr_off;
     half8_t vf[2][kOut], pf[2];

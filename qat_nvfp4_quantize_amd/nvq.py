@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -119,10 +120,8 @@ _SIGS = [
      [ctypes.POINTER(KvCacheArgs), _P, _P, ctypes.c_int, _I64, _I64, _I64, _I64, _I64, _P, _P, _SZ, _P]),
     ("nvq_kv_gather", ctypes.c_int,
      [ctypes.POINTER(KvCacheArgs), _P, _I64, _P, _P, ctypes.c_int, _P, _SZ, _P]),
-    ("nvq_paged_attention_workspace_bytes", _SZ,
-     [ctypes.POINTER(KvCacheArgs), ctypes.POINTER(PagedAttentionArgs)]),
-    ("nvq_paged_attention", ctypes.c_int,
-     [ctypes.POINTER(KvCacheArgs), ctypes.POINTER(PagedAttentionArgs), _P]),
+    ("nvq_paged_attention_workspace_bytes", _SZ, [ctypes.POINTER(KvCacheArgs), _P]),
+    ("nvq_paged_attention", ctypes.c_int, [ctypes.POINTER(KvCacheArgs), _P, _P]),
 ]
 
 EXPORTED = [s[0] for s in _SIGS]
@@ -724,18 +723,20 @@ def nvq_paged_attention(q, cache, cu_q, kv_len, block_table, max_q=None, scale=N
     if lse is not None:
         _typed(lse, "lse", torch.float32, T, Hq)
     _on(dev, q=q, cu_q=cu_q, kv_len=kv_len, block_table=block_table, out=out, lse=lse, ws=ws)
-    a = PagedAttentionArgs(
-        _ATTENTION_SIZE, T, B, 0 if max_q is None else max_q, Hq, 1 if causal else 0, window,
-        D ** -0.5 if scale is None else scale, q.data_ptr(), ld_t, ld_h, cu_q.data_ptr(),
-        kv_len.data_ptr(), block_table.data_ptr(), width, table_ld, out.data_ptr(), o_t, o_h,
-        None if lse is None else lse.data_ptr(), None, 0)
+    head = (_ATTENTION.size, T, B, 0 if max_q is None else max_q, Hq, 1 if causal else 0, window,
+            D ** -0.5 if scale is None else scale, q.data_ptr(), ld_t, ld_h, cu_q.data_ptr(),
+            kv_len.data_ptr(), block_table.data_ptr(), width, table_ld, out.data_ptr(), o_t, o_h,
+            0 if lse is None else lse.data_ptr())
     L = _lib or load()
-    ref = ctypes.byref(a)
     if ws is None:
-        ws = torch.empty(L.nvq_paged_attention_workspace_bytes(cache._ref, ref), dtype=torch.uint8, device=dev)
-    a.ws, a.ws_bytes = ws.data_ptr(), ws.numel()
-    _call(L.nvq_paged_attention, "nvq_paged_attention", dev, cache._ref, ref)
+        ws = torch.empty(L.nvq_paged_attention_workspace_bytes(cache._ref, _ATTENTION.pack(*head, 0, 0)),
+                         dtype=torch.uint8, device=dev)
+    _call(L.nvq_paged_attention, "nvq_paged_attention", dev, cache._ref,
+          _ATTENTION.pack(*head, ws.data_ptr(), ws.numel()))
     return out
 
 
-_ATTENTION_SIZE = ctypes.sizeof(PagedAttentionArgs)
+# nvq_paged_attention_args as bytes: packing them takes a fifth of the time that
+# filling a ctypes structure does, which a decode step would notice
+_ATTENTION = struct.Struct("@Nqqqiiqf4xPqqPPPqqPqqPPN")
+assert _ATTENTION.size == ctypes.sizeof(PagedAttentionArgs)
