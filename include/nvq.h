@@ -563,7 +563,7 @@ typedef struct nvq_paged_attention_args {
 size_t nvq_paged_attention_workspace_bytes(const nvq_kv_cache* cache,
                                            const nvq_paged_attention_args* args);
 /* Limits: total_q < 2^24, q_heads <= 32768, total_q * q_heads <= 2^30, B <=
- * 65535, B * heads <= 2^22, table_width * page_size <= INT32_MAX,
+ * 65535, B * heads <= 2^21, B * table_width <= 2^30, table_width * page_size <= INT32_MAX,
  * B * (table_width * page_size / 128 + 2) <= INT32_MAX.
  * Errors: NVQ_EINVAL, NVQ_ESHAPE, NVQ_EALIGN, NVQ_EWORKSPACE; nothing is
  * launched then. */

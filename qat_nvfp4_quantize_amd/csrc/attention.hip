@@ -140,6 +140,8 @@ __global__ __launch_bounds__(256) void k_attn_any(AttnParams p) {
     p.lse[(int64_t)row * p.Hq + h] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
+constexpr float kLog2e = 1.44269504088896340736f;
+
 // Host-side checks of the sizes (no HIP call, no pointer of args but sizes).
 int attn_sizes(const nvq_kv_cache* cache, const nvq_paged_attention_args* a, AttnParams& p) {
   if (!cache || cache->struct_size != sizeof(nvq_kv_cache)) return NVQ_EINVAL;
@@ -150,8 +152,10 @@ int attn_sizes(const nvq_kv_cache* cache, const nvq_paged_attention_args* a, Att
   if (cache->heads < 1 || ps < 16 || ps > 65536 || a->q_heads < 1 || a->q_heads > 32768 ||
       a->q_heads % cache->heads)
     return NVQ_ESHAPE;
-  if (a->table_width > INT32_MAX / ps || a->B * cache->heads > (1 << 22) ||
-      a->B * (a->table_width * ps / 128 + 2) > INT32_MAX ||
+  // counted in 32 bits: the keys of a sequence, the pages and 128-key units of
+  // all, the threads of a launch
+  if (a->table_width > INT32_MAX / ps || a->B * a->table_width > (1 << 30) ||
+      a->B * (a->table_width * ps / 128 + 2) > INT32_MAX || a->B * cache->heads > (1 << 21) ||
       a->total_q * a->q_heads > (1 << 30))
     return NVQ_ESHAPE;
   p.total_q = (int)a->total_q, p.B = (int)a->B;
@@ -209,7 +213,7 @@ extern "C" int nvq_paged_attention(const nvq_kv_cache* cache, const nvq_paged_at
   const nvq_paged_attention_args& a = *args;
   const int D = p.c.D;
   if ((a.causal != 0 && a.causal != 1) || a.window < 0 || (a.window > 0 && !a.causal) ||
-      !std::isfinite(a.softmax_scale))
+      !std::isfinite(a.softmax_scale * kLog2e))
     return NVQ_EINVAL;
   p.q_ld_t = a.q_ld_t ? a.q_ld_t : (int64_t)p.Hq * D;
   p.q_ld_h = a.q_ld_h ? a.q_ld_h : D;
@@ -236,8 +240,9 @@ extern "C" int nvq_paged_attention(const nvq_kv_cache* cache, const nvq_paged_at
   if (!a.q || !a.out || !a.cu_q || !a.kv_len || (!a.block_table && a.table_width > 0)) return NVQ_EINVAL;
   p.q = a.q, p.out = a.out, p.lse = a.lse;
   p.cu_q = a.cu_q, p.kv_len = a.kv_len, p.table = a.block_table;
-  p.window = a.window, p.causal = a.causal;
-  p.scale_log2 = a.softmax_scale * 1.44269504088896340736f;
+  p.window = std::min<int64_t>(a.window, INT32_MAX);  // past every key; sums with it stay in range
+  p.causal = a.causal;
+  p.scale_log2 = a.softmax_scale * kLog2e;
   if (plan.use_rows || plan.use_chunk) {
     if (plan.use_rows)
       if (int rc = attn_rows_launch(p, plan.rows, plan.chunk, s)) return rc;

@@ -17,7 +17,6 @@ constexpr int kChunkMinUnits = 4;  // key tiles of a run, where there are so man
 // second pass over the divided tiles.
 constexpr float kWholeTiles = 1.5f;
 
-
 // Keys of row tile qt of sequence s, in 64-key tiles from `base`.
 struct TileRange {
   int64_t base, hi;
@@ -38,14 +37,16 @@ __device__ __forceinline__ TileRange tile_range(const AttnParams& p, const Seq& 
 struct PlanLds {
   int end[1024];  // tile_end of the first 1024 sequences
   int scan[16];
-  int last;
+  int64_t last;
 };
 
-// One workgroup (256 or 1024 threads) plans the call: the row tiles of the sequences (the last rows,
-// which see the most keys, first), the units up to each, and the cuts.
+// One workgroup (256 or 1024 threads) plans the call: the row tiles of the
+// sequences (the last rows, which see the most keys, first), the units up to
+// each, and the cuts.  Row ranges that overlap could name more tiles than the
+// buffers hold: the count is cut there.
 __device__ __forceinline__ void plan_chunks(const AttnParams& p, const ChunkPlan& plan, PlanLds& lds) {
   const int t = threadIdx.x, threads = blockDim.x;
-  auto last = [&](int incl) {  // the workgroup's total of an inclusive scan
+  auto last = [&](int64_t incl) {  // the workgroup's total of an inclusive scan
     __syncthreads();
     if (t == threads - 1) lds.last = incl;
     __syncthreads();
@@ -59,12 +60,12 @@ __device__ __forceinline__ void plan_chunks(const AttnParams& p, const ChunkPlan
       const int64_t rows = (int64_t)s.n * p.g;
       n = rows > plan.min_rows ? (int)((rows + plan.tile_rows - 1) / plan.tile_rows) : 0;
     }
-    const int incl = block_inclusive_scan(n, lds.scan);
-    if (b0 + t < 1024) lds.end[b0 + t] = tiles + incl;
-    if (b0 + t < p.B) plan.tile_end[b0 + t] = tiles + incl;
-    tiles += last(incl);
+    const int64_t incl = tiles + block_inclusive_scan_wide(n, lds.scan);
+    const int end = (int)min<int64_t>(incl, plan.max_tiles);
+    if (b0 + t < 1024) lds.end[b0 + t] = end;
+    if (b0 + t < p.B) plan.tile_end[b0 + t] = end;
+    tiles = (int)last(end);
   }
-  tiles = (int)min<int64_t>(tiles, plan.max_tiles);  // overlapping row ranges could name more
   __threadfence_block();
   __syncthreads();
   auto end_of = [&](int b) { return b < 1024 ? lds.end[b] : plan.tile_end[b]; };
@@ -85,9 +86,9 @@ __device__ __forceinline__ void plan_chunks(const AttnParams& p, const ChunkPlan
       units = tile_range(p, load_seq(p, lo), qt, plan.tile_rows).units;
       plan.tile[i] = make_int2(lo, qt);
     }
-    const int incl = block_inclusive_scan(units, lds.scan);
-    if (i < tiles) plan.unit_end[i] = total + incl;
-    total += last(incl);
+    const int64_t incl = total + block_inclusive_scan_wide(units, lds.scan);
+    if (i < tiles) plan.unit_end[i] = incl;
+    total = last(incl);
   }
   const int64_t workers = max<int64_t>(1, min<int64_t>(plan.workers, total / kChunkMinUnits));
   const bool divide = (float)tiles < kWholeTiles * (float)workers && workers > 1;

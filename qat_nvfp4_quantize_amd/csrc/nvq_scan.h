@@ -46,6 +46,13 @@ __device__ __forceinline__ int block_inclusive_scan(int v, int* s_wave) {
   return wave > 0 ? v + s_wave[wave - 1] : v;
 }
 
+// As above for numbers below 2^31 whose sum may pass 32 bits.
+__device__ __forceinline__ int64_t block_inclusive_scan_wide(int v, int* s_wave) {
+  const int low = block_inclusive_scan(v & 0xFFFF, s_wave);
+  __syncthreads();
+  return low + ((int64_t)block_inclusive_scan(v >> 16, s_wave) << 16);
+}
+
 // Tile table of a row-tiled grouped GEMM: expert e's rows [off[e], off[e + 1])
 // split into bm-row tiles, tile i = (expert, first row), experts in order.
 // s_incl[e] holds the inclusive prefix of the experts' tile counts (set by

@@ -530,14 +530,17 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _under(dev, fn, *args):
+    """fn(*args) with `dev` as the current device."""
+    if torch.cuda.current_device() == dev.index:
+        return fn(*args)
+    with torch.cuda.device(dev.index):
+        return fn(*args)
+
+
 def _call(fn, name, dev, *args):
-    """Calls the library with `dev` as the current device, on its current stream."""
-    index = dev.index
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, _raw_stream(index))
+    """Calls the library on `dev`, on its current stream."""
+    rc = _under(dev, fn, *args, _raw_stream(dev.index))
     if rc != 0:
         raise NvqError(name, rc)
 
@@ -729,8 +732,8 @@ def nvq_paged_attention(q, cache, cu_q, kv_len, block_table, max_q=None, scale=N
             0 if lse is None else lse.data_ptr())
     L = _lib or load()
     if ws is None:
-        ws = torch.empty(L.nvq_paged_attention_workspace_bytes(cache._ref, _ATTENTION.pack(*head, 0, 0)),
-                         dtype=torch.uint8, device=dev)
+        ws = torch.empty(_under(dev, L.nvq_paged_attention_workspace_bytes, cache._ref,
+                                _ATTENTION.pack(*head, 0, 0)), dtype=torch.uint8, device=dev)
     _call(L.nvq_paged_attention, "nvq_paged_attention", dev, cache._ref,
           _ATTENTION.pack(*head, ws.data_ptr(), ws.numel()))
     return out

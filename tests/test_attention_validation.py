@@ -128,6 +128,13 @@ def test_attention_refusals():
     for bad in (dict(q=0x1008), dict(out=0x1002), dict(q_ld_t=1028), dict(q_ld_h=132), dict(out_ld_t=1028),
                 dict(cu_q=0x1002), dict(lse=0x1001), dict(ws=0x1010)):
         assert call(**bad) == -3, bad
+    # products of sizes: rows and heads, sequences and heads, table entries, 128-key units
+    for bad, c in ((dict(total_q=1 << 20, q_heads=1032), None),
+                   (dict(B=32769, q_heads=64, table_width=1), dict(heads=64)),
+                   (dict(B=65535, table_width=16385), None),
+                   (dict(B=64, table_width=2 ** 16 - 1), dict(page_size=65536))):
+        assert call(c=_cache(**c) if c else None, **bad) == -2, bad
+    assert call(softmax_scale=3e38) == -1  # not finite in base 2
     assert call(ws_bytes=255) == -4
     assert call(c=_cache(page_size=8)) == -2 and call(c=_cache(head_dim=520)) == -2 and call(c=_cache(heads=3)) == -2
     assert call(c=_cache(k_scales=0x1008)) == -3

@@ -164,3 +164,25 @@ def test_append_equals_the_quantizer_of_dense_rows():
     assert torch.equal(c.v_codes[:, 0].reshape(-1, D // 2)[:T], codes[1])
     assert torch.equal(c.v_scales[:, 0].transpose(1, 2).reshape(-1, D // 16)[:T], scales[1])
     assert float(c.k_scale[0]) == float(st[0]) and float(c.v_scale[0]) == float(st[1])
+
+
+def test_either_output_may_be_left_out():
+    import ctypes
+
+    import torch
+
+    nvq = _nvq()
+    T, H, D, S = 33, 3, 64, 16
+    cache = _filled(nvq, 6, H, S, D)
+    g = torch.Generator().manual_seed(4)
+    k, v = (torch.randn(T, H, D, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    slots = torch.randperm(6 * S, generator=g)[:T].to(torch.int32).cuda()
+    nvq.nvq_kv_append(cache, k, v, slots)
+    want = nvq.nvq_kv_gather(cache, slots)
+    for i in range(2):
+        got = torch.full((T, H, D), 9.0, dtype=torch.bfloat16, device="cuda")
+        dst = [None, None]
+        dst[i] = got.data_ptr()
+        rc = nvq.load().nvq_kv_gather(ctypes.byref(cache.args), slots.data_ptr(), T, *dst, nvq._dtype_code(got), None,
+                                      0, torch.cuda.current_stream().cuda_stream)
+        assert rc == 0 and torch.equal(got, want[i])

@@ -383,3 +383,188 @@ def test_side_stream_and_shared_workspace_of_two_shapes():
     side.synchronize()
     for x, y in zip(got, want):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,n", [(128, 16, 1, 3), (64, 12, 1, 5), (64, 33, 1, 1), (128, 71, 1, 1),
+                                        (256, 16, 1, 2), (256, 17, 1, 2)])
+def test_rows_of_every_kernel_variant(D, Hq, Hkv, n):
+    """17 to 71 rows per key/value head: between the few-rows variants and past
+    the last, beside single tokens and an empty sequence."""
+    seqs = [(n, 333), (1, 130), (0, 0), (n, 5), (n, 2048)]
+    for S in (16, 256):
+        log(f"[attention] {n * Hq // Hkv} rows a head, D={D} page={S}")
+        _run(ref.Pages([b for _, b in seqs], Hkv, S, D, seed=D + n), seqs, Hq)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("seqs", [
+    [(300, 300), (70, 1500)],              # several row tiles of 128 or 256
+    [(40, 40 + 17 * i) for i in range(9)] + [(1, 600), (150, 150)],
+    [(33, 5000), (200, 260)],              # few row tiles: their keys divided
+    [(64, 64)] * 60,                       # many: handed out whole
+])
+def test_many_rows_divided_or_whole(D, seqs):
+    log(f"[attention] D={D} {len(seqs)} sequences, first {seqs[:3]}")
+    Hq = 4 if len(seqs) > 20 else 8
+    pages = ref.Pages([b for _, b in seqs], 2, 64, D, seed=len(seqs))
+    _run(pages, seqs, Hq)
+    if len(seqs) < 20:
+        _run(pages, seqs, Hq, window=130)
+
+
+@pytest.mark.parametrize("B,D,new", [(70, 128, 1), (300, 64, 2), (1100, 64, 1)])
+def test_many_sequences(B, D, new):
+    """More sequences than one step of the planning scans holds, empty ones among them."""
+    log(f"[attention] {B} sequences D={D}")
+    seqs = [(0 if i % 7 == 3 else new, (i * 37) % 150 + new) for i in range(B)]
+    pages = ref.Pages([b for _, b in seqs], 1, 16, D, seed=B)
+    _run(pages, seqs, 2)
+    some = [(40 if i % 97 == 5 else n, max(b, 40)) for i, (n, b) in enumerate(seqs)]
+    _run(ref.Pages([b for _, b in some], 1, 16, D, seed=B + 1), some, 2)
+
+
+def test_pages_larger_than_a_tile():
+    for S in (512, 4096):
+        seqs = [(1, 5000), (70, 900), (3, 513), (130, 4097)]
+        for D in (64, 128, 256):
+            log(f"[attention] page={S} D={D}")
+            _run(ref.Pages([b for _, b in seqs], 1, S, D, seed=S + D), seqs, 2)
+
+
+@pytest.mark.parametrize("n,Hq", [(1, 4), (60, 4), (100, 8)])
+@pytest.mark.parametrize("D", [64, 128, 256, 48])
+@pytest.mark.parametrize("order", ["rising", "falling", "peak"])
+def test_moving_reference(D, n, Hq, order):
+    """Scores that climb by hundreds over the keys, so that the running
+    reference moves and the sums are rescaled many times; that fall from the
+    first key on; and one large score in the middle."""
+    import torch
+
+    length = 700
+    log(f"[attention] {order} scores D={D} n={n}")
+    pages = ref.Pages([length, length], 2, 16, D, seed=n + D)
+    pages.k_codes &= 0x77  # magnitudes only: with positive queries all scores are positive
+    for b in range(2):
+        j = np.arange(length)
+        climb = {"rising": j * 48 // length, "falling": 48 - j * 48 // length,
+                 "peak": np.where(j == 333, 48, 4)}[order]
+        pg, off = pages.table[b, j // 16], j % 16
+        pages.k_scales[pg, :, off] = (0x10 + climb).astype(np.uint8)[:, None, None]
+    nvq = _nvq()
+    seqs = [(n, length), (n, length)]
+    q, cu, lens = _batch(seqs, Hq, D, 5)
+    q = q.abs()
+    args = [torch.from_numpy(x).cuda() for x in (cu, lens, pages.table)]
+    for scale in (2.0, 30.0):
+        out = nvq.nvq_paged_attention(q.cuda(), pages.cache(nvq), *args, max_q=n, scale=scale)
+        out = out.float().cpu().numpy().astype(np.float64)
+        qn = q.float().numpy().astype(np.float64)
+        for b in range(2):
+            k, v = pages.rows(b, length)
+            want, _, tol = ref.attention(qn[cu[b]:cu[b + 1]], k, v, length - n, scale, True, 0)
+            assert (np.abs(out[cu[b]:cu[b + 1]] - want) <= tol).all(), (b, scale)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31, 2 ** 63 - 1])
+def test_windows_past_every_length(window):
+    import torch
+
+    nvq = _nvq()
+    for D, seqs in ((128, [(3, 1), (2, 200)]), (128, [(60, 58), (2, 90)]), (48, [(3, 1), (2, 60)])):
+        pages = ref.Pages([b for _, b in seqs], 1, 16, D, seed=3)
+        q, cu, lens = _batch(seqs, 4, D, 8)
+        args = [q.cuda(), pages.cache(nvq)] + [torch.from_numpy(x).cuda() for x in (cu, lens, pages.table)]
+        a = nvq.nvq_paged_attention(*args)
+        b = nvq.nvq_paged_attention(*args, window=window)
+        assert torch.equal(a, b), (D, seqs)
+
+
+def test_row_ranges_that_overlap_stay_in_bounds():
+    """cu_q that falls and rises again: more row tiles than the rows make.  The
+    buffers hold, the status word tells, rows of one owner are right."""
+    import torch
+
+    nvq = _nvq()
+    n = 200
+    seqs = [(n, 300)] * 5
+    for D, Hq in ((128, 4), (64, 2), (256, 2), (48, 2)):
+        log(f"[attention] overlapping rows D={D}")
+        pages = ref.Pages([300] * 5, 1, 16, D, seed=D)
+        q = torch.randn(2 * n, Hq, D, device="cuda").to(torch.bfloat16)
+        cache = pages.cache(nvq)
+        lens = torch.full((5,), 300, dtype=torch.int32, device="cuda")
+        table = torch.from_numpy(pages.table).cuda()
+
+        def run(cu):
+            ws = nvq.workspace(64 << 20, "cuda")
+            out = torch.full_like(q, 5.0)
+            cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+            nvq.nvq_paged_attention(q, cache, cu, lens, table, max_q=n, ws=ws, out=out)
+            return out, nvq.device_status(ws)
+
+        clean, status = run([0, n, n, n, n, 2 * n])
+        assert status == 0
+        out, status = run([n, 2 * n, 0, n, 0, n])
+        assert status == nvq.NVQ_STATUS_BAD_SEQUENCE
+        out, status = run([0, n, 0, n, 0, n])
+        assert status == nvq.NVQ_STATUS_BAD_SEQUENCE and (out[n:] == 5.0).all()
+
+
+def test_two_captured_graphs_share_a_workspace():
+    """A prompt-chunk call and a decode call captured apart over one workspace,
+    replayed in turn with eager calls on it between them."""
+    import torch
+
+    nvq = _nvq()
+    seqs = [(90, 700), (40, 2100), (1, 33)]
+    pages = ref.Pages([b for _, b in seqs], 2, 64, 128, seed=14)
+    cache = pages.cache(nvq)
+    lens, table = torch.tensor([700, 2100, 33], dtype=torch.int32).cuda(), torch.from_numpy(pages.table).cuda()
+    big = torch.empty(131, 8, 128, dtype=torch.bfloat16, device="cuda")
+    one = torch.empty(3, 8, 128, dtype=torch.bfloat16, device="cuda")
+    cb, co = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 90, 130, 131], [0, 1, 2, 3]))
+    ws = nvq.workspace(256 << 20, "cuda")
+
+    def chunk():
+        return nvq.nvq_paged_attention(big, cache, cb, lens, table, max_q=90, ws=ws)
+
+    def decode():
+        return nvq.nvq_paged_attention(one, cache, co, lens, table, max_q=1, ws=ws)
+
+    graphs, outs = [], []
+    for f in (chunk, decode):
+        big.normal_(), one.normal_()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            f()
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(f())
+        graphs.append(g)
+    for i in range(4):
+        big.normal_(), one.normal_()
+        want = chunk().clone(), decode().clone()
+        ws.fill_(0x7F if i % 2 else 0xFF)
+        for k in ((0, 1), (1, 0), (0, 0), (1, 1))[i]:
+            graphs[k].replay()
+            if i % 2:
+                torch.cuda.synchronize()
+            assert torch.equal(outs[k], want[k]), (i, k)
+        assert nvq.device_status(ws) == 0
+
+
+def test_equal_calls_give_equal_bits():
+    import torch
+
+    nvq = _nvq()
+    for seqs in ([(1, 4000), (1, 9), (1, 700)], [(80, 3000), (1, 500), (200, 900)]):
+        pages = ref.Pages([b for _, b in seqs], 2, 16, 128, seed=6)
+        q, cu, lens = _batch(seqs, 8, 128, 2)
+        args = [q.cuda(), pages.cache(nvq)] + [torch.from_numpy(x).cuda() for x in (cu, lens, pages.table)]
+        n = max(a for a, _ in seqs)
+        first = nvq.nvq_paged_attention(*args, max_q=n)
+        for _ in range(5):
+            assert torch.equal(nvq.nvq_paged_attention(*args, max_q=n)[:cu[-1]], first[:cu[-1]])
