@@ -729,7 +729,7 @@ class KvLeg:
 
 
 def profiled_traffic(profile="quantize_sweep_8192x7168_bf16.txt",
-                     sources=("quantize.hip", "nvq_device.h", "nvq_internal.h")):
+                     sources=("quantize.hip", "nvq_device.h", "nvq_internal.h", "nvq_quant_block.h")):
     """HBM bytes per call from a committed rocprofv3 FETCH_SIZE/WRITE_SIZE
     summary (copy-calibrated), when the kernel sources still hash to the value
     recorded there; else None (the figure is stale once the kernel changes)."""
@@ -892,7 +892,7 @@ def main():
                                    "traffic": profiled_traffic(
                                        "moe_grouped_gemm_decode_prefill.txt",
                                        ("gemm_w4a4.hip", "nvq_device.h", "nvq_internal.h",
-                                        "nvq_scan.h")) if moe_main[0].name == "moe_prefill" else None,
+                                        "nvq_scan.h", "nvq_dequant.h")) if moe_main[0].name == "moe_prefill" else None,
                                    "frac_of_fp4_peak": r["gemm_frac_fp4_peak"]}
     if any(l.name == "copy" for l in legs):
         c = next(l for l in legs if l.name == "copy")

@@ -1,9 +1,10 @@
 // Attention over the paged NVFP4 cache for sequences of many query rows per
-// key/value head (prompt chunks): bound by the matrix cores and the softmax's
-// exponentials, so a tile of keys is dequantized once for 128 rows.
+// key/value head (prompt chunks): compute-bound, so a tile of keys is
+// dequantized once for 128 or 256 rows.
 //
 // A workgroup takes 128 (token, head-of-the-group) rows of one sequence and
-// key/value head, a wave 32 of them, over 64 keys at a time.  The keys' codes
+// key/value head (256 at head dimension 128), a wave 32 of them, over 64 keys
+// at a time.  The keys' codes
 // come into registers one tile ahead, are dequantized exactly to fp16 and
 // written row-major to LDS (K and V alike, double-buffered, one barrier a
 // tile).  Products run transposed (32x32x16 fp16): S^T = K Q^T leaves a lane
@@ -11,6 +12,14 @@
 // V^T P^T; the A operand comes out of the row-major V tile through LDS
 // transpose reads.  The softmax reference moves only when a score exceeds it
 // by 15 (powers of two), as in the few-rows kernel.
+//
+// Measured: two chunks of 4096 tokens behind 4096 and 2562 keys, 32 heads on 8
+// of 128, 720 us, 1.0 PFLOP/s.  The same products and operand reads in a loop
+// of their own, with six vector operations a product, reach 1.4 (the products
+// alone 1.5): with such operands the card lowers its clock, so what counts is
+// the number of operations, and orders of them that overlap better (the next
+// tile's scores under this one's softmax, operands read three steps ahead, 64
+// rows a wave, a barrier every second tile) measured 0 to 10 % slower.
 //
 // Where there are few row tiles, their key tiles are dealt to the workgroups
 // that the chip holds in equal runs (planned on the device from cu_q and
@@ -193,213 +202,213 @@ __global__ __launch_bounds__(64 * W, chunk_wgs_per_cu(D, W) * W / 4) void k_attn
 
 #pragma unroll 1
   for (; x < x_end; ++tile) {
-  // made anew for each tile, as in the few-rows kernel
-  int lane = threadIdx.x & 63;
-  asm volatile("" : "+v"(lane));
-  const int l32 = lane & 31, h = lane >> 5;
-  const int b = __builtin_amdgcn_readfirstlane(plan.tile[tile].x), qt = __builtin_amdgcn_readfirstlane(plan.tile[tile].y);
-  const Seq s = load_seq(p, b);
-  const TileRange range = tile_range(p, s, qt, kTileRows);
-  const int64_t tile_x = plan.unit_end[tile] - range.units;  // its first unit
-  const int u_begin = (int)(x - tile_x), u_end = (int)min<int64_t>(range.units, x_end - tile_x);
-  // slot 0: the part that starts a run; 1: one that ends it and began within
-  const bool whole = u_begin == 0 && u_end == range.units;
-  const int64_t slot = 2 * (int64_t)run + (x != x_begin);
-  x = tile_x + u_end;
-  const int32_t* table = p.table + b * p.table_ld;
+    // made anew for each tile, as in the few-rows kernel
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int l32 = lane & 31, h = lane >> 5;
+    const int b = __builtin_amdgcn_readfirstlane(plan.tile[tile].x), qt = __builtin_amdgcn_readfirstlane(plan.tile[tile].y);
+    const Seq s = load_seq(p, b);
+    const TileRange range = tile_range(p, s, qt, kTileRows);
+    const int64_t tile_x = plan.unit_end[tile] - range.units;  // its first unit
+    const int u_begin = (int)(x - tile_x), u_end = (int)min<int64_t>(range.units, x_end - tile_x);
+    // slot 0: the part that starts a run; 1: one that ends it and began within
+    const bool whole = u_begin == 0 && u_end == range.units;
+    const int64_t slot = 2 * (int64_t)run + (x != x_begin);
+    x = tile_x + u_end;
+    const int32_t* table = p.table + b * p.table_ld;
 
-  // this lane's query row
-  const int64_t rows = (int64_t)s.n * p.g, r = (int64_t)qt * kTileRows + 32 * wave + l32;
-  const bool live = r >= 0 && r < rows;
-  const int qi = live ? (int)(r / p.g) : 0, qh = kvh * p.g + (live ? (int)(r % p.g) : 0);
-  half8_t qf[kSteps];
-  float cq;
-  {
-    const uint16_t* at = p.q + (s.row0 + qi) * p.q_ld_t + qh * p.q_ld_h + 8 * h;
-    uint32_t w[kSteps][4], top = 0;
+    // this lane's query row
+    const int64_t rows = (int64_t)s.n * p.g, r = (int64_t)qt * kTileRows + 32 * wave + l32;
+    const bool live = r >= 0 && r < rows;
+    const int qi = live ? (int)(r / p.g) : 0, qh = kvh * p.g + (live ? (int)(r % p.g) : 0);
+    half8_t qf[kSteps];
+    float cq;
+    {
+      const uint16_t* at = p.q + (s.row0 + qi) * p.q_ld_t + qh * p.q_ld_h + 8 * h;
+      uint32_t w[kSteps][4], top = 0;
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-      const uint4 x = *reinterpret_cast<const uint4*>(at + 16 * u);
-      w[u][0] = x.x, w[u][1] = x.y, w[u][2] = x.z, w[u][3] = x.w;
+      for (int u = 0; u < kSteps; ++u) {
+        const uint4 x = *reinterpret_cast<const uint4*>(at + 16 * u);
+        w[u][0] = x.x, w[u][1] = x.y, w[u][2] = x.z, w[u][3] = x.w;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) top = max(top, max(w[u][j] << 16 & 0x7FFF0000u, w[u][j] & 0x7FFF0000u));
-    }
-    top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-    // as in the few-rows kernel; the sign of the factor goes into Q, so that
-    // the largest product is the largest score, and a factor of 0 too
-    const int ex = (int)(top >> 23);
-    const int shift = (top == 0u || ex == 255) ? 0 : 14 + 127 - max(ex, 1);
-    const float c0 = __builtin_ldexpf(k_factor, -shift);
-    const float sign = c0 < 0.0f ? -1.0f : c0 > 0.0f ? 1.0f : 0.0f;
-    cq = c0 == 0.0f ? 1.0f : fabsf(c0);
-#pragma unroll
-    for (int u = 0; u < kSteps; ++u)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        qf[u][2 * j] = (_Float16)(__builtin_ldexpf(bf16_lo(w[u][j]), shift) * sign);
-        qf[u][2 * j + 1] = (_Float16)(__builtin_ldexpf(bf16_hi(w[u][j]), shift) * sign);
+        for (int j = 0; j < 4; ++j) top = max(top, max(w[u][j] << 16 & 0x7FFF0000u, w[u][j] & 0x7FFF0000u));
       }
-  }
-  int64_t lo64, hi64;
-  visible(p, s, s.pos0 + qi, lo64, hi64);
-  const int see_lo = (int)min<int64_t>(lo64, INT32_MAX), see_hi = live ? (int)max<int64_t>(hi64, 0) : 0;
-  // every row of the wave sees all of [all_lo, all_hi)
-  const int64_t r0 = (int64_t)qt * kTileRows + 32 * wave;
-  int64_t all_lo, all_hi, x64;
-  visible(p, s, s.pos0 + min(r0, rows - 1) / p.g, x64, all_hi);
-  visible(p, s, s.pos0 + min(r0 + 31, rows - 1) / p.g, all_lo, x64);
-
-  floatx16_t o[kOut];
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+      // as in the few-rows kernel; the sign of the factor goes into Q, so that
+      // the largest product is the largest score, and a factor of 0 too
+      const int ex = (int)(top >> 23);
+      const int shift = (top == 0u || ex == 255) ? 0 : 14 + 127 - max(ex, 1);
+      const float c0 = __builtin_ldexpf(k_factor, -shift);
+      const float sign = c0 < 0.0f ? -1.0f : c0 > 0.0f ? 1.0f : 0.0f;
+      cq = c0 == 0.0f ? 1.0f : fabsf(c0);
 #pragma unroll
-  for (int i = 0; i < kOut; ++i) o[i] = (floatx16_t)(0.0f);
-  float ref = -INFINITY, ref_safe = 0.0f, l = 0.0f;
-
-  // Loader: a wave takes 64 / W keys of the tile, a thread 1 / W of one of
-  // them, the 16 lanes of an LDS access keys 4 apart.  Page ids of the wave's
-  // next 64 tiles with one load (-1: no key, or an id outside the cache).
-  const int part = lane & (W - 1);
-  const int key = W == 4 ? 4 * ((lane >> 2) & 3) + (lane >> 4) : 4 * ((lane >> 3) & 1) + (lane >> 4);
-  const int lkey_at = Lds::at(64 / W * wave + key);
-  const int64_t base = range.base + 64 / W * wave;
-  int ids = -1, ids_at = u_begin;
-  auto fetch_ids = [&](int u0) {
-    const int64_t first = base + (int64_t)(u0 + lane) * kTileKeys;
-    const int id = (u0 + lane < u_end && first < range.hi) ? table[first >> p.c.log_ps] : -1;
-    ids = id < p.c.num_pages ? id : -1;
-    ids_at = u0;
-  };
-  TileRegs<D, W> regs;
-  int id;
-  auto fetch = [&](int u) {  // past the last tile: page 0, never looked at
-    if (u - ids_at >= 64) fetch_ids(u);
-    id = __builtin_amdgcn_readlane(ids, u - ids_at);
-    load_tile<D, W>(p, regs, id, kvh, (int)(base + (int64_t)u * kTileKeys) & (p.c.ps - 1), key, part);
-  };
-  auto put = [&](int buf) {
-    store_tile<D, W>(regs, lds.k[buf] + lkey_at, lds.v[buf] + lkey_at, part);
-    if (lane == 0 && wave % (W / 4) == 0) lds.dead[buf][wave / (W / 4)] = id < 0;
-  };
-  fetch_ids(u_begin);
-  fetch(u_begin);
-  put(0);
-  __syncthreads();
-
-  // lane's source address of a transpose read: key 4 h + s / 4, elements
-  // 16 (lane / 16 % 2) + 4 (s % 4), s = lane % 16
-  const int tr_off = Lds::at(4 * h + ((lane & 15) >> 2)) + 2 * (16 * ((lane >> 4) & 1) + 4 * (lane & 3));
-#pragma unroll 1
-  for (int u = u_begin; u < u_end; ++u) {
-    const int buf = (u - u_begin) & 1;
-    const int64_t kb = range.base + (int64_t)u * kTileKeys;
-    fetch(u + 1);
-    floatx16_t sc[2];
-    const uint8_t* k_at = lds.k[buf] + Lds::at(l32) + 16 * h;
-    sc[0] = sc[1] = (floatx16_t)(0.0f);
-    // Operands of the next two steps are read before the products of these:
-    // left alone the compiler puts each read right before its product and
-    // waits for it.
-    half8_t kf[2][4];
-    auto read_k = [&](half8_t (&f)[4], int w) {
+      for (int u = 0; u < kSteps; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        f[i] = *reinterpret_cast<const half8_t*>(k_at + 8 * (i & 1) * Lds::kRow + 32 * (w + (i >> 1)));
-    };
-    read_k(kf[0], 0);
-#pragma unroll
-    for (int w = 0; w < kSteps; w += 2) {
-      if (w + 2 < kSteps) read_k(kf[(w >> 1 & 1) ^ 1], w + 2);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)  // two chains of products in turn
-        sc[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[w >> 1 & 1][i], qf[w + (i >> 1)], sc[i & 1], 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    const uint4 dead = *reinterpret_cast<const uint4*>(lds.dead[buf]);
-    if (kb < all_lo || kb + kTileKeys > all_hi || (dead.x | dead.y | dead.z | dead.w)) {
-#pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int k = 32 * kt + 8 * (v >> 2) + 4 * h + (v & 3), key = (int)kb + k;
-          const uint32_t none = 2 * kt + (v >> 3) == 0 ? dead.x : 2 * kt + (v >> 3) == 1 ? dead.y
-                                : 2 * kt + (v >> 3) == 2 ? dead.z : dead.w;
-          sc[kt][v] = (key >= see_lo && key < see_hi && !none) ? sc[kt][v] : -INFINITY;
+        for (int j = 0; j < 4; ++j) {
+          qf[u][2 * j] = (_Float16)(__builtin_ldexpf(bf16_lo(w[u][j]), shift) * sign);
+          qf[u][2 * j + 1] = (_Float16)(__builtin_ldexpf(bf16_hi(w[u][j]), shift) * sign);
         }
     }
-    float top = max3(sc[0][0], sc[1][0], sc[1][1]), top2 = max3(sc[0][1], sc[0][2], sc[1][2]);
-#pragma unroll
-    for (int v = 3; v < 15; v += 2) {
-      top = max3(top, sc[0][v], sc[1][v]);
-      top2 = max3(top2, sc[0][v + 1], sc[1][v + 1]);
-    }
-    top = max3(top, sc[0][15], sc[1][15]);
-    top = fmaxf(top, top2);
-    top *= cq;
-    if (__ballot(top > ref + kRefRoom)) {
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const float moved = top > ref + kRefRoom ? top - kRefStart : ref;
-      const float keep = moved == ref ? 1.0f : __builtin_amdgcn_exp2f(ref - moved);
-      ref = moved;
-      ref_safe = moved == -INFINITY ? 0.0f : moved;
-      l *= keep;
-      rescale<D == 256>(o, keep);
-    }
-    const NVQ_LDS char* vt = (const NVQ_LDS char*)lds.v[buf] + tr_off;
-    half8_t vf[2][kOut], pf[2];
-    auto read_v = [&](half8_t (&f)[kOut], int j) {
-#pragma unroll
-      for (int i = 0; i < kOut; ++i) f[i] = tr_pair(vt + 4 * j * Lds::kRow + 64 * i, 2 * Lds::kRow);
-    };
-    auto weights = [&](half8_t& f, int j) {  // of 16 keys
-#pragma unroll
-      for (int v = 0; v < 8; ++v) {
-        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j >> 1][8 * (j & 1) + v], cq, -ref_safe));
-        l += w;
-        f[v] = (_Float16)w;
-      }
-    };
-    read_v(vf[0], 0);
-    weights(pf[0], 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j < 3) read_v(vf[(j & 1) ^ 1], j + 1);
-      if (j < 3)
-        weights(pf[(j & 1) ^ 1], j + 1);
-      else
-        put(buf ^ 1);
-#pragma unroll
-      for (int i = 0; i < kOut; ++i)
-        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[j & 1][i], pf[j & 1], o[i], 0, 0, 0);
-    }
-    __syncthreads();
-  }
+    int64_t lo64, hi64;
+    visible(p, s, s.pos0 + qi, lo64, hi64);
+    const int see_lo = (int)min<int64_t>(lo64, INT32_MAX), see_hi = live ? (int)max<int64_t>(hi64, 0) : 0;
+    // every row of the wave sees all of [all_lo, all_hi)
+    const int64_t r0 = (int64_t)qt * kTileRows + 32 * wave;
+    int64_t all_lo, all_hi, x64;
+    visible(p, s, s.pos0 + min(r0, rows - 1) / p.g, x64, all_hi);
+    visible(p, s, s.pos0 + min(r0 + 31, rows - 1) / p.g, all_lo, x64);
 
-  l += __shfl_xor(l, 32, 64);
-  if (whole) {
-    if (live) {
-      const float inv = l == 0.0f ? 0.0f : v_st / l;
-      uint16_t* out = p.out + (s.row0 + qi) * p.out_ld_t + qh * p.out_ld_h;
+    floatx16_t o[kOut];
+#pragma unroll
+    for (int i = 0; i < kOut; ++i) o[i] = (floatx16_t)(0.0f);
+    float ref = -INFINITY, ref_safe = 0.0f, l = 0.0f;
+
+    // Loader: a wave takes 64 / W keys of the tile, a thread 1 / W of one of
+    // them, the 16 lanes of an LDS access keys 4 apart.  Page ids of the wave's
+    // next 64 tiles with one load (-1: no key, or an id outside the cache).
+    const int part = lane & (W - 1);
+    const int key = W == 4 ? 4 * ((lane >> 2) & 3) + (lane >> 4) : 4 * ((lane >> 3) & 1) + (lane >> 4);
+    const int lkey_at = Lds::at(64 / W * wave + key);
+    const int64_t base = range.base + 64 / W * wave;
+    int ids = -1, ids_at = u_begin;
+    auto fetch_ids = [&](int u0) {
+      const int64_t first = base + (int64_t)(u0 + lane) * kTileKeys;
+      const int id = (u0 + lane < u_end && first < range.hi) ? table[first >> p.c.log_ps] : -1;
+      ids = id < p.c.num_pages ? id : -1;
+      ids_at = u0;
+    };
+    TileRegs<D, W> regs;
+    int id;
+    auto fetch = [&](int u) {  // past the last tile: page 0, never looked at
+      if (u - ids_at >= 64) fetch_ids(u);
+      id = __builtin_amdgcn_readlane(ids, u - ids_at);
+      load_tile<D, W>(p, regs, id, kvh, (int)(base + (int64_t)u * kTileKeys) & (p.c.ps - 1), key, part);
+    };
+    auto put = [&](int buf) {
+      store_tile<D, W>(regs, lds.k[buf] + lkey_at, lds.v[buf] + lkey_at, part);
+      if (lane == 0 && wave % (W / 4) == 0) lds.dead[buf][wave / (W / 4)] = id < 0;
+    };
+    fetch_ids(u_begin);
+    fetch(u_begin);
+    put(0);
+    __syncthreads();
+
+    // lane's source address of a transpose read: key 4 h + s / 4, elements
+    // 16 (lane / 16 % 2) + 4 (s % 4), s = lane % 16
+    const int tr_off = Lds::at(4 * h + ((lane & 15) >> 2)) + 2 * (16 * ((lane >> 4) & 1) + 4 * (lane & 3));
+#pragma unroll 1
+    for (int u = u_begin; u < u_end; ++u) {
+      const int buf = (u - u_begin) & 1;
+      const int64_t kb = range.base + (int64_t)u * kTileKeys;
+      fetch(u + 1);
+      floatx16_t sc[2];
+      const uint8_t* k_at = lds.k[buf] + Lds::at(l32) + 16 * h;
+      sc[0] = sc[1] = (floatx16_t)(0.0f);
+      // Operands of the next two steps are read before the products of these:
+      // left alone the compiler puts each read right before its product and
+      // waits for it.
+      half8_t kf[2][4];
+      auto read_k = [&](half8_t (&f)[4], int w) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          f[i] = *reinterpret_cast<const half8_t*>(k_at + 8 * (i & 1) * Lds::kRow + 32 * (w + (i >> 1)));
+      };
+      read_k(kf[0], 0);
+#pragma unroll
+      for (int w = 0; w < kSteps; w += 2) {
+        if (w + 2 < kSteps) read_k(kf[(w >> 1 & 1) ^ 1], w + 2);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // two chains of products in turn
+          sc[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[w >> 1 & 1][i], qf[w + (i >> 1)], sc[i & 1], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      const uint4 dead = *reinterpret_cast<const uint4*>(lds.dead[buf]);
+      if (kb < all_lo || kb + kTileKeys > all_hi || (dead.x | dead.y | dead.z | dead.w)) {
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int k = 32 * kt + 8 * (v >> 2) + 4 * h + (v & 3), key = (int)kb + k;
+            const uint32_t none = 2 * kt + (v >> 3) == 0 ? dead.x : 2 * kt + (v >> 3) == 1 ? dead.y
+                                  : 2 * kt + (v >> 3) == 2 ? dead.z : dead.w;
+            sc[kt][v] = (key >= see_lo && key < see_hi && !none) ? sc[kt][v] : -INFINITY;
+          }
+      }
+      float top = max3(sc[0][0], sc[1][0], sc[1][1]), top2 = max3(sc[0][1], sc[0][2], sc[1][2]);
+#pragma unroll
+      for (int v = 3; v < 15; v += 2) {
+        top = max3(top, sc[0][v], sc[1][v]);
+        top2 = max3(top2, sc[0][v + 1], sc[1][v + 1]);
+      }
+      top = max3(top, sc[0][15], sc[1][15]);
+      top = fmaxf(top, top2);
+      top *= cq;
+      if (__ballot(top > ref + kRefRoom)) {
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float moved = top > ref + kRefRoom ? top - kRefStart : ref;
+        const float keep = moved == ref ? 1.0f : __builtin_amdgcn_exp2f(ref - moved);
+        ref = moved;
+        ref_safe = moved == -INFINITY ? 0.0f : moved;
+        l *= keep;
+        rescale<D == 256>(o, keep);
+      }
+      const NVQ_LDS char* vt = (const NVQ_LDS char*)lds.v[buf] + tr_off;
+      half8_t vf[2][kOut], pf[2];
+      auto read_v = [&](half8_t (&f)[kOut], int j) {
+#pragma unroll
+        for (int i = 0; i < kOut; ++i) f[i] = tr_pair(vt + 4 * j * Lds::kRow + 64 * i, 2 * Lds::kRow);
+      };
+      auto weights = [&](half8_t& f, int j) {  // of 16 keys
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j >> 1][8 * (j & 1) + v], cq, -ref_safe));
+          l += w;
+          f[v] = (_Float16)w;
+        }
+      };
+      read_v(vf[0], 0);
+      weights(pf[0], 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j < 3) read_v(vf[(j & 1) ^ 1], j + 1);
+        if (j < 3)
+          weights(pf[(j & 1) ^ 1], j + 1);
+        else
+          put(buf ^ 1);
+#pragma unroll
+        for (int i = 0; i < kOut; ++i)
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[j & 1][i], pf[j & 1], o[i], 0, 0, 0);
+      }
+      __syncthreads();
+    }
+
+    l += __shfl_xor(l, 32, 64);
+    if (whole) {
+      if (live) {
+        const float inv = l == 0.0f ? 0.0f : v_st / l;
+        uint16_t* out = p.out + (s.row0 + qi) * p.out_ld_t + qh * p.out_ld_h;
+#pragma unroll
+        for (int i = 0; i < kOut; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            *reinterpret_cast<uint2*>(out + 32 * i + 8 * v + 4 * h) =
+                make_uint2(f32_to_bf16_any(o[i][4 * v] * inv) | (f32_to_bf16_any(o[i][4 * v + 1] * inv) << 16),
+                           f32_to_bf16_any(o[i][4 * v + 2] * inv) | (f32_to_bf16_any(o[i][4 * v + 3] * inv) << 16));
+        if (p.lse && h == 0)
+          p.lse[(int64_t)(s.row0 + qi) * p.Hq + qh] = l == 0.0f ? -INFINITY : (ref + __builtin_log2f(l)) * kLn2;
+      }
+    } else {
+      const int64_t at = (slot * p.c.H + kvh) * kTileRows + 32 * wave + l32;
+      float* out = plan.part_o + at * D;
 #pragma unroll
       for (int i = 0; i < kOut; ++i)
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-          *reinterpret_cast<uint2*>(out + 32 * i + 8 * v + 4 * h) =
-              make_uint2(f32_to_bf16_any(o[i][4 * v] * inv) | (f32_to_bf16_any(o[i][4 * v + 1] * inv) << 16),
-                         f32_to_bf16_any(o[i][4 * v + 2] * inv) | (f32_to_bf16_any(o[i][4 * v + 3] * inv) << 16));
-      if (p.lse && h == 0)
-        p.lse[(int64_t)(s.row0 + qi) * p.Hq + qh] = l == 0.0f ? -INFINITY : (ref + __builtin_log2f(l)) * kLn2;
+          *reinterpret_cast<float4*>(out + 32 * i + 8 * v + 4 * h) =
+              make_float4(o[i][4 * v], o[i][4 * v + 1], o[i][4 * v + 2], o[i][4 * v + 3]);
+      if (h == 0) plan.part_ml[at] = make_float2(ref, l);
     }
-  } else {
-    const int64_t at = (slot * p.c.H + kvh) * kTileRows + 32 * wave + l32;
-    float* out = plan.part_o + at * D;
-#pragma unroll
-    for (int i = 0; i < kOut; ++i)
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        *reinterpret_cast<float4*>(out + 32 * i + 8 * v + 4 * h) =
-            make_float4(o[i][4 * v], o[i][4 * v + 1], o[i][4 * v + 2], o[i][4 * v + 3]);
-    if (h == 0) plan.part_ml[at] = make_float2(ref, l);
-  }
   }
 }
 

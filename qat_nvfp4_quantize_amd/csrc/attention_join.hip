@@ -123,7 +123,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnParams p, RowsPlan rows, 
   const int tile = chunk.run_tile[w];
   const int64_t end = chunk.unit_end[tile], start = tile ? chunk.unit_end[tile - 1] : 0;
   if (w * total / runs == start) return;  // between two tiles
-  const int64_t w0 = ((start + 1) * runs - 1) / total, w1 = (end * runs - 1) / total;  // runs of its first and last unit
+  // runs of its first and last unit
+  const int64_t w0 = ((start + 1) * runs - 1) / total, w1 = (end * runs - 1) / total;
   const int64_t first = 2 * w0 + (w0 * total / runs != start);
   const int2 bq = chunk.tile[tile];
   const Seq s = load_seq(p, bq.x);

@@ -26,8 +26,12 @@
 // cu_q and kv_len itself; each of a workgroup's four waves takes 32 keys of a
 // unit).  A run may end inside a sequence: the parts of such sequences are
 // joined by a second kernel.  Equal runs matter: with pieces cut per sequence
-// 64 ragged sequences made 1232 pieces for 768 places, two rounds of 33 us
-// (83 us the call).
+// 64 ragged sequences made 1232 pieces for 768 places, two rounds of 33 us.
+//
+// Measured: 64 sequences of up to 8192 keys, 32 heads on 8 of 128: 78 us (a
+// copy moves the same bytes in 63), of which the loop takes 57 at 5.6 TB/s, the
+// rest goes to finding the runs, the first loads and the join; one sequence of
+// 131072 keys: 45 us (30).
 
 #include <hip/hip_runtime.h>
 
@@ -158,8 +162,10 @@ __device__ __forceinline__ void v_operands(const uint32_t (&w)[8], const half2_t
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t e0 = fp4_pair_f16<kSel>(w[2 * i]), e1 = fp4_pair_f16<kSel>(w[2 * i + 1]);
-    a[i] = __builtin_bit_cast(uint32_t, (half2_t)(__builtin_bit_cast(half2_t, __builtin_amdgcn_perm(e1, e0, 0x05040100u)) * sc[i]));
-    b[i] = __builtin_bit_cast(uint32_t, (half2_t)(__builtin_bit_cast(half2_t, __builtin_amdgcn_perm(e1, e0, 0x07060302u)) * sc[i]));
+    const half2_t x = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(e1, e0, 0x05040100u)) * sc[i];
+    const half2_t y = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(e1, e0, 0x07060302u)) * sc[i];
+    a[i] = __builtin_bit_cast(uint32_t, x);
+    b[i] = __builtin_bit_cast(uint32_t, y);
   }
   __builtin_memcpy(&lo, a, 16);
   __builtin_memcpy(&hi, b, 16);
@@ -171,7 +177,8 @@ __device__ __forceinline__ half2_t scale_two(uint32_t four, int i) {
 }
 
 template <int D, int MT>
-__global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnParams p, RowsPlan plan, ChunkPlan chunks) {
+__global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnParams p, RowsPlan plan,
+                                                                           ChunkPlan chunks) {
   constexpr int kRows = 16 * MT, kTiles = D / 16, kSteps = D / 32;
   constexpr int kPitch = D + 4;  // floats; 16-byte rows shifted over the banks
   __shared__ float s_o[2][kRows * kPitch];
@@ -234,242 +241,242 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
     }
     if (x != x_begin) __syncthreads();  // the last sequence's LDS reads are done
     x = seq_x + u_end;
-  const int rows = s.n * p.g;
-  const int32_t* table = p.table + b * p.table_ld;
+    const int rows = s.n * p.g;
+    const int32_t* table = p.table + b * p.table_ld;
 
-  // Q in fp16 under a power of two per row that brings its largest magnitude
-  // to 2^14 .. 2^15: bf16's 8 bits are kept down to 2^-38 of it.
-  half8_t qf[MT][kSteps];
-  float cq[MT];
-  int see_lo[MT], see_hi[MT];
+    // Q in fp16 under a power of two per row that brings its largest magnitude
+    // to 2^14 .. 2^15: bf16's 8 bits are kept down to 2^-38 of it.
+    half8_t qf[MT][kSteps];
+    float cq[MT];
+    int see_lo[MT], see_hi[MT];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int r = 16 * mt + n, i = r / p.g, h = kvh * p.g + (r - i * p.g);
-    const bool live = r < rows;
-    uint32_t w[kSteps][4];
-    uint32_t top = 0;
-    const uint16_t* at = p.q + (s.row0 + (live ? i : 0)) * p.q_ld_t + (live ? h : 0) * p.q_ld_h + q * (D / 4);
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r = 16 * mt + n, i = r / p.g, h = kvh * p.g + (r - i * p.g);
+      const bool live = r < rows;
+      uint32_t w[kSteps][4];
+      uint32_t top = 0;
+      const uint16_t* at = p.q + (s.row0 + (live ? i : 0)) * p.q_ld_t + (live ? h : 0) * p.q_ld_h + q * (D / 4);
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-      const uint4 x = *reinterpret_cast<const uint4*>(at + 8 * u);
-      w[u][0] = live ? x.x : 0u, w[u][1] = live ? x.y : 0u, w[u][2] = live ? x.z : 0u, w[u][3] = live ? x.w : 0u;
+      for (int u = 0; u < kSteps; ++u) {
+        const uint4 x = *reinterpret_cast<const uint4*>(at + 8 * u);
+        w[u][0] = live ? x.x : 0u, w[u][1] = live ? x.y : 0u, w[u][2] = live ? x.z : 0u, w[u][3] = live ? x.w : 0u;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) top = max(top, max(w[u][j] << 16 & 0x7FFF0000u, w[u][j] & 0x7FFF0000u));
-    }
-    top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-    const int ex = (int)(top >> 23);
-    const int shift = (top == 0u || ex == 255) ? 0 : 14 + 127 - max(ex, 1);
-#pragma unroll
-    for (int u = 0; u < kSteps; ++u)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        qf[mt][u][2 * j] = (_Float16)__builtin_ldexpf(bf16_lo(w[u][j]), shift);
-        qf[mt][u][2 * j + 1] = (_Float16)__builtin_ldexpf(bf16_hi(w[u][j]), shift);
+        for (int j = 0; j < 4; ++j) top = max(top, max(w[u][j] << 16 & 0x7FFF0000u, w[u][j] & 0x7FFF0000u));
       }
-    cq[mt] = __builtin_ldexpf(c0, -shift);
-    int64_t lo, hi;
-    visible(p, s, s.pos0 + i, lo, hi);
-    see_lo[mt] = (int)min<int64_t>(lo, INT32_MAX);
-    see_hi[mt] = live ? (int)max<int64_t>(hi, 0) : 0;
-  }
-  // every row sees all of [all_lo, all_hi)
-  int64_t all_lo, all_hi, x64;
-  visible(p, s, s.pos0, x64, all_hi);
-  visible(p, s, s.pos0 + s.n - 1, all_lo, x64);
-
-  floatx4_t o[MT][kTiles];
-  float ref[MT], ref_safe[MT], l[MT];
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+      const int ex = (int)(top >> 23);
+      const int shift = (top == 0u || ex == 255) ? 0 : 14 + 127 - max(ex, 1);
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    ref[mt] = -INFINITY, ref_safe[mt] = 0.0f, l[mt] = 0.0f;
+      for (int u = 0; u < kSteps; ++u)
 #pragma unroll
-    for (int u = 0; u < kTiles; ++u) o[mt][u] = (floatx4_t)(0.0f);
-  }
-
-  // Page ids of the wave's next 32 steps, one load: lane 2 i + t has those of
-  // step i's half t (-1: no key, or an id outside the cache).
-  int ids = -1, ids_at = u_begin;
-  auto fetch_ids = [&](int u0) {
-    const int64_t key = range.base + (int64_t)(u0 + (lane >> 1)) * kUnit + 32 * wave + 16 * (lane & 1);
-    int id = key < range.hi ? table[key >> p.c.log_ps] : -1;
-    if (id >= p.c.num_pages) id = -1;
-    ids = id;
-    ids_at = u0;
-  };
-  auto page_pair = [&](int u, int (&id)[2]) {
-    if (u - ids_at >= 32) fetch_ids(u);
-    id[0] = __builtin_amdgcn_readlane(ids, 2 * (u - ids_at));
-    id[1] = __builtin_amdgcn_readlane(ids, 2 * (u - ids_at) + 1);
-  };
-
-  const int64_t base = range.base + 32 * wave;
-  auto fetch = [&](StepRegs<D>& regs, int (&id)[2], int u) {
-    page_pair(u, id);
-    load_step<D>(p, regs, id, kvh, (int)((base + (int64_t)u * kUnit) & (p.c.ps - 1)), lane);
-  };
-  auto consume = [&](const StepRegs<D>& cur, const int (&id)[2], int u) {
-    const int64_t kb = base + (int64_t)u * kUnit;
-    if (kb < range.hi) {
-      floatx4_t sc[MT][2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const uint32_t ks = cur.ks[t] & 0x7F7F7F7Fu;  // finite for any byte
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) sc[mt][t] = (floatx4_t)(0.0f);
-#pragma unroll
-        for (int w = 0; w < kSteps; ++w) {
-          const half8_t a = dequant8(cur.k[t][w], scale_pair(ks, w >> 1));
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            sc[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qf[mt][w], sc[mt][t], 0, 0, 0);
+        for (int j = 0; j < 4; ++j) {
+          qf[mt][u][2 * j] = (_Float16)__builtin_ldexpf(bf16_lo(w[u][j]), shift);
+          qf[mt][u][2 * j + 1] = (_Float16)__builtin_ldexpf(bf16_hi(w[u][j]), shift);
         }
-      }
-      const bool whole = kb >= all_lo && kb + 32 <= all_hi && id[0] >= 0 && id[1] >= 0;
-      half8_t pf[MT];
+      cq[mt] = __builtin_ldexpf(c0, -shift);
+      int64_t lo, hi;
+      visible(p, s, s.pos0 + i, lo, hi);
+      see_lo[mt] = (int)min<int64_t>(lo, INT32_MAX);
+      see_hi[mt] = live ? (int)max<int64_t>(hi, 0) : 0;
+    }
+    // every row sees all of [all_lo, all_hi)
+    int64_t all_lo, all_hi, x64;
+    visible(p, s, s.pos0, x64, all_hi);
+    visible(p, s, s.pos0 + s.n - 1, all_lo, x64);
+
+    floatx4_t o[MT][kTiles];
+    float ref[MT], ref_safe[MT], l[MT];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float top = -INFINITY;
+    for (int mt = 0; mt < MT; ++mt) {
+      ref[mt] = -INFINITY, ref_safe[mt] = 0.0f, l[mt] = 0.0f;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+      for (int u = 0; u < kTiles; ++u) o[mt][u] = (floatx4_t)(0.0f);
+    }
+
+    // Page ids of the wave's next 32 steps, one load: lane 2 i + t has those of
+    // step i's half t (-1: no key, or an id outside the cache).
+    int ids = -1, ids_at = u_begin;
+    auto fetch_ids = [&](int u0) {
+      const int64_t key = range.base + (int64_t)(u0 + (lane >> 1)) * kUnit + 32 * wave + 16 * (lane & 1);
+      int id = key < range.hi ? table[key >> p.c.log_ps] : -1;
+      if (id >= p.c.num_pages) id = -1;
+      ids = id;
+      ids_at = u0;
+    };
+    auto page_pair = [&](int u, int (&id)[2]) {
+      if (u - ids_at >= 32) fetch_ids(u);
+      id[0] = __builtin_amdgcn_readlane(ids, 2 * (u - ids_at));
+      id[1] = __builtin_amdgcn_readlane(ids, 2 * (u - ids_at) + 1);
+    };
+
+    const int64_t base = range.base + 32 * wave;
+    auto fetch = [&](StepRegs<D>& regs, int (&id)[2], int u) {
+      page_pair(u, id);
+      load_step<D>(p, regs, id, kvh, (int)((base + (int64_t)u * kUnit) & (p.c.ps - 1)), lane);
+    };
+    auto consume = [&](const StepRegs<D>& cur, const int (&id)[2], int u) {
+      const int64_t kb = base + (int64_t)u * kUnit;
+      if (kb < range.hi) {
+        floatx4_t sc[MT][2];
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            float x = sc[mt][t][v] * cq[mt];
-            if (!whole) {
-              const int key = (int)kb + 16 * t + 4 * q + v;
-              x = (key >= see_lo[mt] && key < see_hi[mt] && id[t] >= 0) ? x : -INFINITY;
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t ks = cur.ks[t] & 0x7F7F7F7Fu;  // finite for any byte
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) sc[mt][t] = (floatx4_t)(0.0f);
+#pragma unroll
+          for (int w = 0; w < kSteps; ++w) {
+            const half8_t a = dequant8(cur.k[t][w], scale_pair(ks, w >> 1));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              sc[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qf[mt][w], sc[mt][t], 0, 0, 0);
+          }
+        }
+        const bool whole = kb >= all_lo && kb + 32 <= all_hi && id[0] >= 0 && id[1] >= 0;
+        half8_t pf[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              float x = sc[mt][t][v] * cq[mt];
+              if (!whole) {
+                const int key = (int)kb + 16 * t + 4 * q + v;
+                x = (key >= see_lo[mt] && key < see_hi[mt] && id[t] >= 0) ? x : -INFINITY;
+              }
+              sc[mt][t][v] = x;
+              top = fmaxf(top, x);
             }
-            sc[mt][t][v] = x;
-            top = fmaxf(top, x);
+          if (__ballot(top > ref[mt] + kRefRoom)) {
+            top = fmaxf(top, __shfl_xor(top, 16, 64));
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const float moved = top > ref[mt] + kRefRoom ? top - kRefStart : ref[mt];
+            const float keep = moved == ref[mt] ? 1.0f : __builtin_amdgcn_exp2f(ref[mt] - moved);
+            ref[mt] = moved;
+            ref_safe[mt] = moved == -INFINITY ? 0.0f : moved;
+            l[mt] *= keep;
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) o[mt][i] *= keep;
           }
-        if (__ballot(top > ref[mt] + kRefRoom)) {
-          top = fmaxf(top, __shfl_xor(top, 16, 64));
-          top = fmaxf(top, __shfl_xor(top, 32, 64));
-          const float moved = top > ref[mt] + kRefRoom ? top - kRefStart : ref[mt];
-          const float keep = moved == ref[mt] ? 1.0f : __builtin_amdgcn_exp2f(ref[mt] - moved);
-          ref[mt] = moved;
-          ref_safe[mt] = moved == -INFINITY ? 0.0f : moved;
-          l[mt] *= keep;
 #pragma unroll
-          for (int i = 0; i < kTiles; ++i) o[mt][i] *= keep;
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const float w = __builtin_amdgcn_exp2f(sc[mt][t][v] - ref_safe[mt]);
+              l[mt] += w;
+              pf[mt][4 * t + v] = (_Float16)w;
+            }
         }
+        half2_t vs[4];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int i = 0; i < 4; ++i) vs[i] = scale_two(cur.vs[i >> 1] & 0x7F7F7F7Fu, i & 1);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const float w = __builtin_amdgcn_exp2f(sc[mt][t][v] - ref_safe[mt]);
-            l[mt] += w;
-            pf[mt][4 * t + v] = (_Float16)w;
+        for (int j = 0; j < StepRegs<D>::kVW; ++j) {
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = cur.v[i][j];
+          half8_t a[8];
+          v_operands<0>(w, vs, a[0], a[1]);
+          v_operands<1>(w, vs, a[2], a[3]);
+          if constexpr (D > 64) {
+            v_operands<2>(w, vs, a[4], a[5]);
+            v_operands<3>(w, vs, a[6], a[7]);
           }
-      }
-      half2_t vs[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) vs[i] = scale_two(cur.vs[i >> 1] & 0x7F7F7F7Fu, i & 1);
+          for (int e = 0; e < (D > 64 ? 8 : 4); ++e)
 #pragma unroll
-      for (int j = 0; j < StepRegs<D>::kVW; ++j) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = cur.v[i][j];
-        half8_t a[8];
-        v_operands<0>(w, vs, a[0], a[1]);
-        v_operands<1>(w, vs, a[2], a[3]);
-        if constexpr (D > 64) {
-          v_operands<2>(w, vs, a[4], a[5]);
-          v_operands<3>(w, vs, a[6], a[7]);
+            for (int mt = 0; mt < MT; ++mt)
+              o[mt][8 * j + e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[e], pf[mt], o[mt][8 * j + e], 0, 0, 0);
         }
-#pragma unroll
-        for (int e = 0; e < (D > 64 ? 8 : 4); ++e)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            o[mt][8 * j + e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[e], pf[mt], o[mt][8 * j + e], 0, 0, 0);
       }
-    }
-  };
-  // the next step's loads are in flight while a step is computed
-  StepRegs<D> cur, nxt;
-  int id_cur[2], id_nxt[2];
-  fetch_ids(u_begin);
-  fetch(cur, id_cur, u_begin);
+    };
+    // the next step's loads are in flight while a step is computed
+    StepRegs<D> cur, nxt;
+    int id_cur[2], id_nxt[2];
+    fetch_ids(u_begin);
+    fetch(cur, id_cur, u_begin);
 #pragma unroll 1
-  for (int u = u_begin; u < u_end; ++u) {
-    if (u + 1 < u_end) fetch(nxt, id_nxt, u + 1);
-    consume(cur, id_cur, u);
-    cur = nxt;
-    id_cur[0] = id_nxt[0], id_cur[1] = id_nxt[1];
-  }
+    for (int u = u_begin; u < u_end; ++u) {
+      if (u + 1 < u_end) fetch(nxt, id_nxt, u + 1);
+      consume(cur, id_cur, u);
+      cur = nxt;
+      id_cur[0] = id_nxt[0], id_cur[1] = id_nxt[1];
+    }
 
-  // Join the four waves: each scales its part to the common reference, waves
-  // 2 and 3 hand theirs over through LDS, waves 0 and 1 add and leave two
-  // parts for the workgroup.
+    // Join the four waves: each scales its part to the common reference, waves
+    // 2 and 3 hand theirs over through LDS, waves 0 and 1 add and leave two
+    // parts for the workgroup.
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    l[mt] += __shfl_xor(l[mt], 16, 64);
-    l[mt] += __shfl_xor(l[mt], 32, 64);
-    if (q == 0) s_m[wave][16 * mt + n] = ref[mt], s_l[wave][16 * mt + n] = l[mt];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int r = 16 * mt + n;
-    const float m = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
-    const float f = ref[mt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ref[mt] - m);
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) o[mt][i] *= f;
-  }
-  float* part = s_o[wave & 1];
-  auto each = [&](auto&& f) {  // float4 of 4 consecutive elements of the lane's row
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-#pragma unroll
-        for (int i = 0; i < kTiles / 4; ++i)
-          f(reinterpret_cast<float4*>(part + (16 * mt + n) * kPitch + (4 * q + v) * kTiles + 4 * i),
-            make_float4(o[mt][4 * i][v], o[mt][4 * i + 1][v], o[mt][4 * i + 2][v], o[mt][4 * i + 3][v]));
-  };
-  if (wave >= 2) each([](float4* at, float4 x) { *at = x; });
-  __syncthreads();
-  if (wave < 2)
-    each([](float4* at, float4 x) {
-      const float4 y = *at;
-      *at = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-    });
-  __syncthreads();
-  constexpr int kChunks = D / 8;
-  for (int e = threadIdx.x; e < kRows * kChunks; e += 256) {
-    const int r = e / kChunks, ch = e - r * kChunks;
-    if (r >= rows) break;
-    const float m = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
-    float sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w)
-      sum += s_m[w][r] == -INFINITY ? 0.0f : s_l[w][r] * __builtin_amdgcn_exp2f(s_m[w][r] - m);
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 a = *reinterpret_cast<const float4*>(s_o[0] + r * kPitch + 8 * ch + 4 * i);
-      const float4 b = *reinterpret_cast<const float4*>(s_o[1] + r * kPitch + 8 * ch + 4 * i);
-      x[4 * i] = a.x + b.x, x[4 * i + 1] = a.y + b.y, x[4 * i + 2] = a.z + b.z, x[4 * i + 3] = a.w + b.w;
+    for (int mt = 0; mt < MT; ++mt) {
+      l[mt] += __shfl_xor(l[mt], 16, 64);
+      l[mt] += __shfl_xor(l[mt], 32, 64);
+      if (q == 0) s_m[wave][16 * mt + n] = ref[mt], s_l[wave][16 * mt + n] = l[mt];
     }
-    if (whole_seq) {
-      const int i = r / p.g, h = kvh * p.g + (r - i * p.g);
-      const float inv = sum == 0.0f ? 0.0f : v_st / sum;
-      uint32_t w[4];
+    __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = f32_to_bf16_any(x[2 * j] * inv) | (f32_to_bf16_any(x[2 * j + 1] * inv) << 16);
-      *reinterpret_cast<uint4*>(p.out + (s.row0 + i) * p.out_ld_t + h * p.out_ld_h + 8 * ch) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-      if (p.lse && ch == 0)
-        p.lse[(int64_t)(s.row0 + i) * p.Hq + h] = sum == 0.0f ? -INFINITY : (m + __builtin_log2f(sum)) * kLn2;
-    } else {
-      const int64_t at_row = ((int64_t)slot * p.c.H + kvh) * kRows + r;
-      float4* at = reinterpret_cast<float4*>(plan.part_o + at_row * D + 8 * ch);
-      at[0] = make_float4(x[0], x[1], x[2], x[3]);
-      at[1] = make_float4(x[4], x[5], x[6], x[7]);
-      if (ch == 0) plan.part_ml[at_row] = make_float2(m, sum);
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r = 16 * mt + n;
+      const float m = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+      const float f = ref[mt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ref[mt] - m);
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) o[mt][i] *= f;
     }
-  }
+    float* part = s_o[wave & 1];
+    auto each = [&](auto&& f) {  // float4 of 4 consecutive elements of the lane's row
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+          for (int i = 0; i < kTiles / 4; ++i)
+            f(reinterpret_cast<float4*>(part + (16 * mt + n) * kPitch + (4 * q + v) * kTiles + 4 * i),
+              make_float4(o[mt][4 * i][v], o[mt][4 * i + 1][v], o[mt][4 * i + 2][v], o[mt][4 * i + 3][v]));
+    };
+    if (wave >= 2) each([](float4* at, float4 x) { *at = x; });
+    __syncthreads();
+    if (wave < 2)
+      each([](float4* at, float4 x) {
+        const float4 y = *at;
+        *at = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+      });
+    __syncthreads();
+    constexpr int kChunks = D / 8;
+    for (int e = threadIdx.x; e < kRows * kChunks; e += 256) {
+      const int r = e / kChunks, ch = e - r * kChunks;
+      if (r >= rows) break;
+      const float m = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        sum += s_m[w][r] == -INFINITY ? 0.0f : s_l[w][r] * __builtin_amdgcn_exp2f(s_m[w][r] - m);
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 a = *reinterpret_cast<const float4*>(s_o[0] + r * kPitch + 8 * ch + 4 * i);
+        const float4 b = *reinterpret_cast<const float4*>(s_o[1] + r * kPitch + 8 * ch + 4 * i);
+        x[4 * i] = a.x + b.x, x[4 * i + 1] = a.y + b.y, x[4 * i + 2] = a.z + b.z, x[4 * i + 3] = a.w + b.w;
+      }
+      if (whole_seq) {
+        const int i = r / p.g, h = kvh * p.g + (r - i * p.g);
+        const float inv = sum == 0.0f ? 0.0f : v_st / sum;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = f32_to_bf16_any(x[2 * j] * inv) | (f32_to_bf16_any(x[2 * j + 1] * inv) << 16);
+        *reinterpret_cast<uint4*>(p.out + (s.row0 + i) * p.out_ld_t + h * p.out_ld_h + 8 * ch) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+        if (p.lse && ch == 0)
+          p.lse[(int64_t)(s.row0 + i) * p.Hq + h] = sum == 0.0f ? -INFINITY : (m + __builtin_log2f(sum)) * kLn2;
+      } else {
+        const int64_t at_row = ((int64_t)slot * p.c.H + kvh) * kRows + r;
+        float4* at = reinterpret_cast<float4*>(plan.part_o + at_row * D + 8 * ch);
+        at[0] = make_float4(x[0], x[1], x[2], x[3]);
+        at[1] = make_float4(x[4], x[5], x[6], x[7]);
+        if (ch == 0) plan.part_ml[at_row] = make_float2(m, sum);
+      }
+    }
   }
 }
 
@@ -493,8 +500,9 @@ void attn_rows_plan(const AttnParams& p, int tiles, bool chunks, WsCarve& ws, Ro
   plan.max_rows = 16 * tiles;
   const int64_t units = (p.num_keys + kUnit - 1) / kUnit + 1;  // most of a sequence
   const int64_t places = (int64_t)rows_wgs_per_cu(p.c.D, tiles) * device_cu_count();
-  plan.workers =
-      units * p.B <= kFewUnits ? 1 : (int)std::max<int64_t>(1, std::min((places - 1 - chunks) / p.c.H, units * p.B / kMinUnits));
+  plan.workers = 1;
+  if (units * p.B > kFewUnits)
+    plan.workers = (int)std::max<int64_t>(1, std::min((places - 1 - chunks) / p.c.H, units * p.B / kMinUnits));
   plan.may_split = plan.workers > 1;
   plan.seq = ws.take<int32_t>(2 * (size_t)p.B);
   const size_t rows = plan.may_split ? (size_t)(2 * plan.workers * p.c.H) * plan.max_rows : 0;

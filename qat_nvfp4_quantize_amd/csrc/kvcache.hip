@@ -1,8 +1,8 @@
 // Paged NVFP4 KV cache: new K and V tokens quantized as they are written into
 // their slots, and slots read back.
 //
-// Both kernels are HBM-bound (2 or 4 bytes a value against 0.5625).  A workgroup takes consecutive tokens of one
-// head, and workgroups are numbered heads first: they go to the eight XCDs in
+// Both kernels are HBM-bound (2 or 4 bytes a value against 0.5625).  A
+// workgroup takes consecutive tokens of one head, and workgroups are numbered heads first: they go to the eight XCDs in
 // turn, so with 8 heads (or 4) an XCD sees one head (or half of its tokens).
 // A token's V scales are single bytes in lines that the head's other slots
 // share; kept to one L2 they are merged there.  32768 tokens of 8 heads x 128
@@ -126,7 +126,8 @@ __global__ __launch_bounds__(kKvThreads) void k_kv_gather(KvGatherParams p) {
         const int64_t tile = ((int64_t)(slot[i] >> p.c.log_ps) * p.c.H + h) << p.c.log_ps;
         const uint8_t* at = (is_v ? p.c.v_codes : p.c.k_codes) + (tile + off) * (p.c.D >> 1) + vec * (kN / 2);
         w[i] = kBF16 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
-        sc[i] = is_v ? p.c.v_scales[tile * nb + ((int64_t)blk << p.c.log_ps) + off] : p.c.k_scales[(tile + off) * nb + blk];
+        sc[i] = is_v ? p.c.v_scales[tile * nb + ((int64_t)blk << p.c.log_ps) + off]
+                     : p.c.k_scales[(tile + off) * nb + blk];
       } else if (slot[i] >= 0) {
         bad = (uint32_t)NVQ_STATUS_BAD_SLOT;
       }

@@ -1,5 +1,5 @@
-// Workgroup-wide integer prefix sum for the small tables of the GEMM entry
-// points (tile tables over at most 1024 experts).
+// Prefix sums of a wave and of a workgroup, and the tile tables of the grouped
+// GEMM entry points (at most 1024 experts).
 #pragma once
 
 #include <hip/hip_runtime.h>
