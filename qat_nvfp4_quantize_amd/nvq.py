@@ -6,6 +6,7 @@ the library is missing or the device is not a GPU, calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -528,19 +529,18 @@ def qat_fakequant_gemm_w4a16(mode, w_codes, w_scales, w_tensor_scale, expert_off
 _HEAD_TYPES = (torch.bfloat16, torch.float32)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _under(dev, fn, *args):
-    """fn(*args) with `dev` as the current device."""
-    if torch.cuda.current_device() == dev.index:
-        return fn(*args)
-    with torch.cuda.device(dev.index):
-        return fn(*args)
+_HERE = contextlib.nullcontext()
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(fn, name, dev, *args):
-    """Calls the library on `dev`, on its current stream."""
-    rc = _under(dev, fn, *args, _raw_stream(dev.index))
+    """Calls the library with `dev` as the current device, on its current stream."""
+    index = dev.index
+    if _current_device() == index:
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
     if rc != 0:
         raise NvqError(name, rc)
 
@@ -597,7 +597,7 @@ def nvq_rope(x, positions, inv_freq, interleaved=False, magnitude=1.0, inverse=F
     dev = x.device
     old_t = old_h = 0
     if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         if out.shape != x.shape or out.dtype != x.dtype:
             raise ValueError("out must have the shape and dtype of x")
@@ -718,7 +718,7 @@ def nvq_paged_attention(q, cache, cu_q, kv_len, block_table, max_q=None, scale=N
             raise ValueError("block_table must have unit column stride and rows that do not overlap")
     o_t = o_h = 0
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         if out.shape != q.shape:
             raise ValueError("out must have the shape of q")
@@ -732,8 +732,9 @@ def nvq_paged_attention(q, cache, cu_q, kv_len, block_table, max_q=None, scale=N
             0 if lse is None else lse.data_ptr())
     L = _lib or load()
     if ws is None:
-        ws = torch.empty(_under(dev, L.nvq_paged_attention_workspace_bytes, cache._ref,
-                                _ATTENTION.pack(*head, 0, 0)), dtype=torch.uint8, device=dev)
+        with torch.cuda.device(dev) if _current_device() != dev.index else _HERE:
+            nbytes = L.nvq_paged_attention_workspace_bytes(cache._ref, _ATTENTION.pack(*head, 0, 0))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _call(L.nvq_paged_attention, "nvq_paged_attention", dev, cache._ref,
           _ATTENTION.pack(*head, ws.data_ptr(), ws.numel()))
     return out
