@@ -221,48 +221,6 @@ __global__ __launch_bounds__(64 * W, chunk_wgs_per_cu(D, W) * W / 4) void k_attn
     const int64_t rows = (int64_t)s.n * p.g, r = (int64_t)qt * kTileRows + 32 * wave + l32;
     const bool live = r >= 0 && r < rows;
     const int qi = live ? (int)(r / p.g) : 0, qh = kvh * p.g + (live ? (int)(r % p.g) : 0);
-    half8_t qf[kSteps];
-    float cq;
-    {
-      const uint16_t* at = p.q + (s.row0 + qi) * p.q_ld_t + qh * p.q_ld_h + 8 * h;
-      uint32_t w[kSteps][4], top = 0;
-#pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        const uint4 x = *reinterpret_cast<const uint4*>(at + 16 * u);
-        w[u][0] = x.x, w[u][1] = x.y, w[u][2] = x.z, w[u][3] = x.w;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) top = max(top, max(w[u][j] << 16 & 0x7FFF0000u, w[u][j] & 0x7FFF0000u));
-      }
-      top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-      // as in the few-rows kernel; the sign of the factor goes into Q, so that
-      // the largest product is the largest score, and a factor of 0 too
-      const int ex = (int)(top >> 23);
-      const int shift = (top == 0u || ex == 255) ? 0 : 14 + 127 - max(ex, 1);
-      const float c0 = __builtin_ldexpf(k_factor, -shift);
-      const float sign = c0 < 0.0f ? -1.0f : c0 > 0.0f ? 1.0f : 0.0f;
-      cq = c0 == 0.0f ? 1.0f : fabsf(c0);
-#pragma unroll
-      for (int u = 0; u < kSteps; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          qf[u][2 * j] = (_Float16)(__builtin_ldexpf(bf16_lo(w[u][j]), shift) * sign);
-          qf[u][2 * j + 1] = (_Float16)(__builtin_ldexpf(bf16_hi(w[u][j]), shift) * sign);
-        }
-    }
-    int64_t lo64, hi64;
-    visible(p, s, s.pos0 + qi, lo64, hi64);
-    const int see_lo = (int)min<int64_t>(lo64, INT32_MAX), see_hi = live ? (int)max<int64_t>(hi64, 0) : 0;
-    // every row of the wave sees all of [all_lo, all_hi)
-    const int64_t r0 = (int64_t)qt * kTileRows + 32 * wave;
-    int64_t all_lo, all_hi, x64;
-    visible(p, s, s.pos0 + min(r0, rows - 1) / p.g, x64, all_hi);
-    visible(p, s, s.pos0 + min(r0 + 31, rows - 1) / p.g, all_lo, x64);
-
-    floatx16_t o[kOut];
-#pragma unroll
-    for (int i = 0; i < kOut; ++i) o[i] = (floatx16_t)(0.0f);
-    float ref = -INFINITY, ref_safe = 0.0f, l = 0.0f;
-
     // Loader: a wave takes 64 / W keys of the tile, a thread 1 / W of one of
     // them, the 16 lanes of an LDS access keys 4 apart.  Page ids of the wave's
     // next 64 tiles with one load (-1: no key, or an id outside the cache).
@@ -288,8 +246,60 @@ __global__ __launch_bounds__(64 * W, chunk_wgs_per_cu(D, W) * W / 4) void k_attn
       store_tile<D, W>(regs, lds.k[buf] + lkey_at, lds.v[buf] + lkey_at, part);
       if (lane == 0 && wave % (W / 4) == 0) lds.dead[buf][wave / (W / 4)] = id < 0;
     };
+    // The first loads go out before any of them is waited for: page ids, the
+    // query row, and the codes of the first tile.
     fetch_ids(u_begin);
+    uint32_t qw[kSteps][4];
+    {
+      const uint16_t* at = p.q + (s.row0 + qi) * p.q_ld_t + qh * p.q_ld_h + 8 * h;
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        const uint4 x = *reinterpret_cast<const uint4*>(at + 16 * u);
+        qw[u][0] = x.x, qw[u][1] = x.y, qw[u][2] = x.z, qw[u][3] = x.w;
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
     fetch(u_begin);
+    __builtin_amdgcn_sched_barrier(0);
+
+    half8_t qf[kSteps];
+    float cq;
+    {
+      uint32_t top = 0;
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, max(qw[u][j] << 16 & 0x7FFF0000u, qw[u][j] & 0x7FFF0000u));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+      // as in the few-rows kernel; the sign of the factor goes into Q, so that
+      // the largest product is the largest score, and a factor of 0 too
+      const int ex = (int)(top >> 23);
+      const int shift = (top == 0u || ex == 255) ? 0 : 14 + 127 - max(ex, 1);
+      const float c0 = __builtin_ldexpf(k_factor, -shift);
+      const float sign = c0 < 0.0f ? -1.0f : c0 > 0.0f ? 1.0f : 0.0f;
+      cq = c0 == 0.0f ? 1.0f : fabsf(c0);
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          qf[u][2 * j] = (_Float16)(__builtin_ldexpf(bf16_lo(qw[u][j]), shift) * sign);
+          qf[u][2 * j + 1] = (_Float16)(__builtin_ldexpf(bf16_hi(qw[u][j]), shift) * sign);
+        }
+    }
+    int64_t lo64, hi64;
+    visible(p, s, s.pos0 + qi, lo64, hi64);
+    const int see_lo = (int)min<int64_t>(lo64, INT32_MAX), see_hi = live ? (int)max<int64_t>(hi64, 0) : 0;
+    // every row of the wave sees all of [all_lo, all_hi)
+    const int64_t r0 = (int64_t)qt * kTileRows + 32 * wave;
+    int64_t all_lo, all_hi, x64;
+    visible(p, s, s.pos0 + min(r0, rows - 1) / p.g, x64, all_hi);
+    visible(p, s, s.pos0 + min(r0 + 31, rows - 1) / p.g, all_lo, x64);
+
+    floatx16_t o[kOut];
+#pragma unroll
+    for (int i = 0; i < kOut; ++i) o[i] = (floatx16_t)(0.0f);
+    float ref = -INFINITY, ref_safe = 0.0f, l = 0.0f;
+
     put(0);
     __syncthreads();
 

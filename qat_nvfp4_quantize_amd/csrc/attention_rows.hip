@@ -244,56 +244,6 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
     const int rows = s.n * p.g;
     const int32_t* table = p.table + b * p.table_ld;
 
-    // Q in fp16 under a power of two per row that brings its largest magnitude
-    // to 2^14 .. 2^15: bf16's 8 bits are kept down to 2^-38 of it.
-    half8_t qf[MT][kSteps];
-    float cq[MT];
-    int see_lo[MT], see_hi[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int r = 16 * mt + n, i = r / p.g, h = kvh * p.g + (r - i * p.g);
-      const bool live = r < rows;
-      uint32_t w[kSteps][4];
-      uint32_t top = 0;
-      const uint16_t* at = p.q + (s.row0 + (live ? i : 0)) * p.q_ld_t + (live ? h : 0) * p.q_ld_h + q * (D / 4);
-#pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        const uint4 x = *reinterpret_cast<const uint4*>(at + 8 * u);
-        w[u][0] = live ? x.x : 0u, w[u][1] = live ? x.y : 0u, w[u][2] = live ? x.z : 0u, w[u][3] = live ? x.w : 0u;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) top = max(top, max(w[u][j] << 16 & 0x7FFF0000u, w[u][j] & 0x7FFF0000u));
-      }
-      top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-      top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-      const int ex = (int)(top >> 23);
-      const int shift = (top == 0u || ex == 255) ? 0 : 14 + 127 - max(ex, 1);
-#pragma unroll
-      for (int u = 0; u < kSteps; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          qf[mt][u][2 * j] = (_Float16)__builtin_ldexpf(bf16_lo(w[u][j]), shift);
-          qf[mt][u][2 * j + 1] = (_Float16)__builtin_ldexpf(bf16_hi(w[u][j]), shift);
-        }
-      cq[mt] = __builtin_ldexpf(c0, -shift);
-      int64_t lo, hi;
-      visible(p, s, s.pos0 + i, lo, hi);
-      see_lo[mt] = (int)min<int64_t>(lo, INT32_MAX);
-      see_hi[mt] = live ? (int)max<int64_t>(hi, 0) : 0;
-    }
-    // every row sees all of [all_lo, all_hi)
-    int64_t all_lo, all_hi, x64;
-    visible(p, s, s.pos0, x64, all_hi);
-    visible(p, s, s.pos0 + s.n - 1, all_lo, x64);
-
-    floatx4_t o[MT][kTiles];
-    float ref[MT], ref_safe[MT], l[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      ref[mt] = -INFINITY, ref_safe[mt] = 0.0f, l[mt] = 0.0f;
-#pragma unroll
-      for (int u = 0; u < kTiles; ++u) o[mt][u] = (floatx4_t)(0.0f);
-    }
-
     // Page ids of the wave's next 32 steps, one load: lane 2 i + t has those of
     // step i's half t (-1: no key, or an id outside the cache).
     int ids = -1, ids_at = u_begin;
@@ -315,6 +265,73 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
       page_pair(u, id);
       load_step<D>(p, regs, id, kvh, (int)((base + (int64_t)u * kUnit) & (p.c.ps - 1)), lane);
     };
+    // The first loads go out before any of them is waited for: page ids, the
+    // query rows, and the codes of the first step.
+    fetch_ids(u_begin);
+    uint32_t qw[MT][kSteps][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r = 16 * mt + n, i = r < rows ? r / p.g : 0, h = kvh * p.g + (r < rows ? r - i * p.g : 0);
+      const uint16_t* at = p.q + (s.row0 + i) * p.q_ld_t + h * p.q_ld_h + q * (D / 4);
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        const uint4 x = *reinterpret_cast<const uint4*>(at + 8 * u);
+        qw[mt][u][0] = x.x, qw[mt][u][1] = x.y, qw[mt][u][2] = x.z, qw[mt][u][3] = x.w;
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    StepRegs<D> cur, nxt;
+    int id_cur[2], id_nxt[2];
+    fetch(cur, id_cur, u_begin);
+    __builtin_amdgcn_sched_barrier(0);
+
+    // Q in fp16 under a power of two per row that brings its largest magnitude
+    // to 2^14 .. 2^15: bf16's 8 bits are kept down to 2^-38 of it.
+    half8_t qf[MT][kSteps];
+    float cq[MT];
+    int see_lo[MT], see_hi[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r = 16 * mt + n;
+      const bool live = r < rows;
+      uint32_t(&w)[kSteps][4] = qw[mt];
+      uint32_t top = 0;
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[u][j] = live ? w[u][j] : 0u, top = max(top, max(w[u][j] << 16 & 0x7FFF0000u, w[u][j] & 0x7FFF0000u));
+      }
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+      const int ex = (int)(top >> 23);
+      const int shift = (top == 0u || ex == 255) ? 0 : 14 + 127 - max(ex, 1);
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          qf[mt][u][2 * j] = (_Float16)__builtin_ldexpf(bf16_lo(w[u][j]), shift);
+          qf[mt][u][2 * j + 1] = (_Float16)__builtin_ldexpf(bf16_hi(w[u][j]), shift);
+        }
+      cq[mt] = __builtin_ldexpf(c0, -shift);
+      int64_t lo, hi;
+      visible(p, s, s.pos0 + r / p.g, lo, hi);
+      see_lo[mt] = (int)min<int64_t>(lo, INT32_MAX);
+      see_hi[mt] = live ? (int)max<int64_t>(hi, 0) : 0;
+    }
+    // every row sees all of [all_lo, all_hi)
+    int64_t all_lo, all_hi, x64;
+    visible(p, s, s.pos0, x64, all_hi);
+    visible(p, s, s.pos0 + s.n - 1, all_lo, x64);
+
+    floatx4_t o[MT][kTiles];
+    float ref[MT], ref_safe[MT], l[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      ref[mt] = -INFINITY, ref_safe[mt] = 0.0f, l[mt] = 0.0f;
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u) o[mt][u] = (floatx4_t)(0.0f);
+    }
+
     auto consume = [&](const StepRegs<D>& cur, const int (&id)[2], int u) {
       const int64_t kb = base + (int64_t)u * kUnit;
       if (kb < range.hi) {
@@ -392,13 +409,8 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
         }
       }
     };
-    // the next step's loads are in flight while a step is computed
-    StepRegs<D> cur, nxt;
-    int id_cur[2], id_nxt[2];
-    fetch_ids(u_begin);
-    fetch(cur, id_cur, u_begin);
 #pragma unroll 1
-    for (int u = u_begin; u < u_end; ++u) {
+    for (int u = u_begin; u < u_end; ++u) {  // the next step's loads are in flight while a step is computed
       if (u + 1 < u_end) fetch(nxt, id_nxt, u + 1);
       consume(cur, id_cur, u);
       cur = nxt;
