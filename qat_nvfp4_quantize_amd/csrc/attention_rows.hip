@@ -28,10 +28,10 @@
 // joined by a second kernel.  Equal runs matter: with pieces cut per sequence
 // 64 ragged sequences made 1232 pieces for 768 places, two rounds of 33 us.
 //
-// Measured: 64 sequences of up to 8192 keys, 32 heads on 8 of 128: 78 us (a
+// Measured: 64 sequences of up to 8192 keys, 32 heads on 8 of 128: 73 us (a
 // copy moves the same bytes in 63), of which the loop takes 57 at 5.6 TB/s, the
 // rest goes to finding the runs, the first loads and the join; one sequence of
-// 131072 keys: 45 us (30).
+// 131072 keys, 64 heads on 8: 43 us (30).
 
 #include <hip/hip_runtime.h>
 
@@ -82,9 +82,9 @@ __device__ __forceinline__ int chunk_units(const AttnParams& p, int max_rows, in
 
 // Units of a workgroup's run, where there are so many; and units of the whole
 // call up to which one workgroup a head takes them all, which spares the
-// joining launch (512 keys of one sequence: 12.0 us against 14.5, most of both
-// the time to launch).
-constexpr int kMinUnits = 2, kFewUnits = 5;
+// joining launch (one sequence of 777 keys: 13.1 us against 15.4, of 1024: 14.2
+// against 15.4, of 1500: 17.7 against 14.8).
+constexpr int kMinUnits = 2, kFewUnits = 10;
 
 // Workgroups of a kernel variant that a CU holds (its register budget).
 constexpr int rows_wgs_per_cu(int D, int MT) {
