@@ -103,7 +103,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnParams p, RowsPlan rows, 
     if (count == 1) return;
     // the first worker's slot as noted, slot 0 of the others
     auto at = [&](int i) {
-      return ((int64_t)(i == 0 ? first : 2 * ((first >> 1) + i)) * p.c.H + kvh) * rows.max_rows + r0;
+      return ((int64_t)(i == 0 ? first : 2 * ((first >> 1) + i)) * p.c.H + kvh) * rows.part_rows + r0;
     };
     auto out_row = [&](int k, int64_t& row, int& head) {
       const int r = r0 + k;

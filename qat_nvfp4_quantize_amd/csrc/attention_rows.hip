@@ -20,13 +20,16 @@
 // by 15 (in powers of two): weights stay within fp16, and a step without a
 // move rescales nothing.
 //
-// Work is split over the keys: per key/value head, the 128-key units of all
-// sequences in one row are dealt to as many workgroups as the chip holds at
-// once, in equal runs, whatever the lengths (every wave finds its run from
-// cu_q and kv_len itself; each of a workgroup's four waves takes 32 keys of a
-// unit).  A run may end inside a sequence: the parts of such sequences are
-// joined by a second kernel.  Equal runs matter: with pieces cut per sequence
-// 64 ragged sequences made 1232 pieces for 768 places, two rounds of 33 us.
+// Work is split over the keys: per key/value head, the units of all sequences
+// in one row are dealt to as many workers as the chip holds at once, in equal
+// runs, whatever the lengths (every wave finds its run from cu_q and kv_len
+// itself).  A worker is a workgroup, each of its four waves taking 32 keys of a
+// 128-key unit, or (W = 1), where there are many sequences, a wave with units
+// of 32: no exchange between waves, a quarter of the set-up of a sequence, but
+// four times the runs, hence more parts.  A run may end inside a sequence: the
+// parts of such sequences are joined by a second kernel.  Equal runs matter:
+// with pieces cut per sequence 64 ragged sequences made 1232 pieces for 768
+// places, two rounds of 33 us.
 //
 // Measured: 64 sequences of up to 8192 keys, 32 heads on 8 of 128: 73 us (a
 // copy moves the same bytes in 63), of which the loop takes 57 at 5.6 TB/s, the
@@ -50,7 +53,8 @@ namespace {
 
 typedef float floatx4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kUnit = 128;      // keys of a workgroup step: 4 waves x 32
+// Keys of a step: 32 of each of a worker's W waves.
+constexpr int unit_keys(int W) { return 32 * W; }
 constexpr float kRefRoom = 15;  // a score may exceed the reference by this (2^15 < fp16's largest)
 constexpr float kRefStart = 9;  // and the reference is set this much below the largest score seen
 
@@ -59,7 +63,9 @@ struct Range {
   int64_t base, hi;
   int units;
 };
+template <int W>
 __device__ __forceinline__ Range key_range(const AttnParams& p, const Seq& s) {
+  constexpr int kUnit = unit_keys(W);
   Range r;
   int64_t lo, x;
   visible(p, s, s.pos0, lo, x);
@@ -70,12 +76,13 @@ __device__ __forceinline__ Range key_range(const AttnParams& p, const Seq& s) {
 }
 
 // Units up to and with sequence 64 c + lane, within its chunk of 64.
+template <int W>
 __device__ __forceinline__ int chunk_units(const AttnParams& p, int max_rows, int c) {
   const int b = 64 * c + (threadIdx.x & 63);
   int units = 0;
   if (b < p.B) {
     const Seq s = load_seq(p, b);
-    if (s.n > 0 && s.n * p.g <= max_rows) units = key_range(p, s).units;
+    if (s.n > 0 && s.n * p.g <= max_rows) units = key_range<W>(p, s).units;
   }
   return wave_inclusive_scan(units);
 }
@@ -176,10 +183,10 @@ __device__ __forceinline__ half2_t scale_two(uint32_t four, int i) {
   return __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0u, four, i ? 0x0C030C02u : 0x0C010C00u) << 7);
 }
 
-template <int D, int MT>
+template <int D, int MT, int W>
 __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnParams p, RowsPlan plan,
                                                                            ChunkPlan chunks) {
-  constexpr int kRows = 16 * MT, kTiles = D / 16, kSteps = D / 32;
+  constexpr int kRows = 16 * MT, kTiles = D / 16, kSteps = D / 32, kUnit = unit_keys(W);
   constexpr int kPitch = D + 4;  // floats; 16-byte rows shifted over the banks
   __shared__ float s_o[2][kRows * kPitch];
   __shared__ float s_m[4][kRows], s_l[4][kRows];
@@ -197,12 +204,13 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
     plan_chunks(p, chunks, s_one.plan);
     return;
   }
-  const int block = blockIdx.x - 1 - plan.plans_chunks, kvh = block % p.c.H, worker = block / p.c.H;
+  const int block = blockIdx.x - 1 - plan.plans_chunks, kvh = block % p.c.H;
+  const int worker = W == 4 ? block / p.c.H : block / p.c.H * 4 + wave, share = W == 4 ? wave : 0;  // share of a unit
 
   // this worker's run [x, x_end) of the units of all sequences
-  int chunk = 0, incl = chunk_units(p, plan.max_rows, 0), total = __builtin_amdgcn_readlane(incl, 63);
-  for (int c = 1; 64 * c < p.B; ++c) total += __builtin_amdgcn_readlane(chunk_units(p, plan.max_rows, c), 63);
-  const int workers = min(plan.workers, max(1, total / kMinUnits));
+  int chunk = 0, incl = chunk_units<W>(p, plan.max_rows, 0), total = __builtin_amdgcn_readlane(incl, 63);
+  for (int c = 1; 64 * c < p.B; ++c) total += __builtin_amdgcn_readlane(chunk_units<W>(p, plan.max_rows, c), 63);
+  const int workers = min(plan.workers, max(1, total / (kMinUnits * 4 / W)));
   if (worker >= workers || total == 0) return;
   int x = (int)((int64_t)worker * total / workers);
   const int x_begin = x, x_end = (int)((int64_t)(worker + 1) * total / workers);
@@ -222,24 +230,24 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
     while (!past) {
       if (64 * (chunk + 1) >= p.B) return;  // only if the arrays change under the call
       before += __builtin_amdgcn_readlane(incl, 63);
-      incl = chunk_units(p, plan.max_rows, ++chunk);
+      incl = chunk_units<W>(p, plan.max_rows, ++chunk);
       past = __ballot(before + incl > x);
     }
     const int sl = __builtin_ctzll(past), b = 64 * chunk + sl;
     const Seq s = load_seq(p, b);
-    const Range range = key_range(p, s);
+    const Range range = key_range<W>(p, s);
     const int seq_x = before + __builtin_amdgcn_readlane(incl, sl) - range.units;  // its first unit
     const int u_begin = x - seq_x, u_end = min(range.units, x_end - seq_x);
     // a part that starts a run goes to the worker's slot 0, one that ends it
     // inside a sequence begun within the run to slot 1
     const bool whole_seq = u_begin == 0 && u_end == range.units;
     const int slot = x == x_begin ? 2 * worker : 2 * worker + 1;
-    if (u_begin == 0 && kvh == 0 && threadIdx.x == 0) {
+    if (u_begin == 0 && kvh == 0 && (W == 4 ? threadIdx.x : threadIdx.x & 63) == 0) {
       const int last = (int)(((int64_t)(seq_x + range.units) * workers - 1) / total);
       plan.seq[2 * b] = slot;
       plan.seq[2 * b + 1] = last - worker + 1;
     }
-    if (x != x_begin) __syncthreads();  // the last sequence's LDS reads are done
+    if (W == 4 && x != x_begin) __syncthreads();  // the last sequence's LDS reads are done
     x = seq_x + u_end;
     const int rows = s.n * p.g;
     const int32_t* table = p.table + b * p.table_ld;
@@ -248,7 +256,7 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
     // step i's half t (-1: no key, or an id outside the cache).
     int ids = -1, ids_at = u_begin;
     auto fetch_ids = [&](int u0) {
-      const int64_t key = range.base + (int64_t)(u0 + (lane >> 1)) * kUnit + 32 * wave + 16 * (lane & 1);
+      const int64_t key = range.base + (int64_t)(u0 + (lane >> 1)) * kUnit + 32 * share + 16 * (lane & 1);
       int id = key < range.hi ? table[key >> p.c.log_ps] : -1;
       if (id >= p.c.num_pages) id = -1;
       ids = id;
@@ -260,7 +268,7 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
       id[1] = __builtin_amdgcn_readlane(ids, 2 * (u - ids_at) + 1);
     };
 
-    const int64_t base = range.base + 32 * wave;
+    const int64_t base = range.base + 32 * share;
     auto fetch = [&](StepRegs<D>& regs, int (&id)[2], int u) {
       page_pair(u, id);
       load_step<D>(p, regs, id, kvh, (int)((base + (int64_t)u * kUnit) & (p.c.ps - 1)), lane);
@@ -299,7 +307,10 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
 #pragma unroll
       for (int u = 0; u < kSteps; ++u) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[u][j] = live ? w[u][j] : 0u, top = max(top, max(w[u][j] << 16 & 0x7FFF0000u, w[u][j] & 0x7FFF0000u));
+        for (int j = 0; j < 4; ++j) {
+          w[u][j] = live ? w[u][j] : 0u;
+          top = max(top, max(w[u][j] << 16 & 0x7FFF0000u, w[u][j] & 0x7FFF0000u));
+        }
       }
       top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
       top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
@@ -417,76 +428,112 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
       id_cur[0] = id_nxt[0], id_cur[1] = id_nxt[1];
     }
 
-    // Join the four waves: each scales its part to the common reference, waves
-    // 2 and 3 hand theirs over through LDS, waves 0 and 1 add and leave two
-    // parts for the workgroup.
+    if constexpr (W == 4) {
+      // Join the four waves: each scales its part to the common reference, waves
+      // 2 and 3 hand theirs over through LDS, waves 0 and 1 add and leave two
+      // parts for the workgroup.
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      l[mt] += __shfl_xor(l[mt], 16, 64);
-      l[mt] += __shfl_xor(l[mt], 32, 64);
-      if (q == 0) s_m[wave][16 * mt + n] = ref[mt], s_l[wave][16 * mt + n] = l[mt];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int r = 16 * mt + n;
-      const float m = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
-      const float f = ref[mt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ref[mt] - m);
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i) o[mt][i] *= f;
-    }
-    float* part = s_o[wave & 1];
-    auto each = [&](auto&& f) {  // float4 of 4 consecutive elements of the lane's row
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-#pragma unroll
-          for (int i = 0; i < kTiles / 4; ++i)
-            f(reinterpret_cast<float4*>(part + (16 * mt + n) * kPitch + (4 * q + v) * kTiles + 4 * i),
-              make_float4(o[mt][4 * i][v], o[mt][4 * i + 1][v], o[mt][4 * i + 2][v], o[mt][4 * i + 3][v]));
-    };
-    if (wave >= 2) each([](float4* at, float4 x) { *at = x; });
-    __syncthreads();
-    if (wave < 2)
-      each([](float4* at, float4 x) {
-        const float4 y = *at;
-        *at = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-      });
-    __syncthreads();
-    constexpr int kChunks = D / 8;
-    for (int e = threadIdx.x; e < kRows * kChunks; e += 256) {
-      const int r = e / kChunks, ch = e - r * kChunks;
-      if (r >= rows) break;
-      const float m = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
-      float sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-        sum += s_m[w][r] == -INFINITY ? 0.0f : s_l[w][r] * __builtin_amdgcn_exp2f(s_m[w][r] - m);
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 a = *reinterpret_cast<const float4*>(s_o[0] + r * kPitch + 8 * ch + 4 * i);
-        const float4 b = *reinterpret_cast<const float4*>(s_o[1] + r * kPitch + 8 * ch + 4 * i);
-        x[4 * i] = a.x + b.x, x[4 * i + 1] = a.y + b.y, x[4 * i + 2] = a.z + b.z, x[4 * i + 3] = a.w + b.w;
+      for (int mt = 0; mt < MT; ++mt) {
+        l[mt] += __shfl_xor(l[mt], 16, 64);
+        l[mt] += __shfl_xor(l[mt], 32, 64);
+        if (q == 0) s_m[wave][16 * mt + n] = ref[mt], s_l[wave][16 * mt + n] = l[mt];
       }
-      if (whole_seq) {
-        const int i = r / p.g, h = kvh * p.g + (r - i * p.g);
-        const float inv = sum == 0.0f ? 0.0f : v_st / sum;
-        uint32_t w[4];
+      __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = f32_to_bf16_any(x[2 * j] * inv) | (f32_to_bf16_any(x[2 * j + 1] * inv) << 16);
-        *reinterpret_cast<uint4*>(p.out + (s.row0 + i) * p.out_ld_t + h * p.out_ld_h + 8 * ch) =
-            make_uint4(w[0], w[1], w[2], w[3]);
-        if (p.lse && ch == 0)
-          p.lse[(int64_t)(s.row0 + i) * p.Hq + h] = sum == 0.0f ? -INFINITY : (m + __builtin_log2f(sum)) * kLn2;
-      } else {
-        const int64_t at_row = ((int64_t)slot * p.c.H + kvh) * kRows + r;
-        float4* at = reinterpret_cast<float4*>(plan.part_o + at_row * D + 8 * ch);
-        at[0] = make_float4(x[0], x[1], x[2], x[3]);
-        at[1] = make_float4(x[4], x[5], x[6], x[7]);
-        if (ch == 0) plan.part_ml[at_row] = make_float2(m, sum);
+      for (int mt = 0; mt < MT; ++mt) {
+        const int r = 16 * mt + n;
+        const float m = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+        const float f = ref[mt] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ref[mt] - m);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) o[mt][i] *= f;
+      }
+      float* part = s_o[wave & 1];
+      auto each = [&](auto&& f) {  // float4 of 4 consecutive elements of the lane's row
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int i = 0; i < kTiles / 4; ++i)
+              f(reinterpret_cast<float4*>(part + (16 * mt + n) * kPitch + (4 * q + v) * kTiles + 4 * i),
+                make_float4(o[mt][4 * i][v], o[mt][4 * i + 1][v], o[mt][4 * i + 2][v], o[mt][4 * i + 3][v]));
+      };
+      if (wave >= 2) each([](float4* at, float4 x) { *at = x; });
+      __syncthreads();
+      if (wave < 2)
+        each([](float4* at, float4 x) {
+          const float4 y = *at;
+          *at = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        });
+      __syncthreads();
+      constexpr int kChunks = D / 8;
+      for (int e = threadIdx.x; e < kRows * kChunks; e += 256) {
+        const int r = e / kChunks, ch = e - r * kChunks;
+        if (r >= rows) break;
+        const float m = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          sum += s_m[w][r] == -INFINITY ? 0.0f : s_l[w][r] * __builtin_amdgcn_exp2f(s_m[w][r] - m);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float4 a = *reinterpret_cast<const float4*>(s_o[0] + r * kPitch + 8 * ch + 4 * i);
+          const float4 b = *reinterpret_cast<const float4*>(s_o[1] + r * kPitch + 8 * ch + 4 * i);
+          x[4 * i] = a.x + b.x, x[4 * i + 1] = a.y + b.y, x[4 * i + 2] = a.z + b.z, x[4 * i + 3] = a.w + b.w;
+        }
+        if (whole_seq) {
+          const int i = r / p.g, h = kvh * p.g + (r - i * p.g);
+          const float inv = sum == 0.0f ? 0.0f : v_st / sum;
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = f32_to_bf16_any(x[2 * j] * inv) | (f32_to_bf16_any(x[2 * j + 1] * inv) << 16);
+          *reinterpret_cast<uint4*>(p.out + (s.row0 + i) * p.out_ld_t + h * p.out_ld_h + 8 * ch) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+          if (p.lse && ch == 0)
+            p.lse[(int64_t)(s.row0 + i) * p.Hq + h] = sum == 0.0f ? -INFINITY : (m + __builtin_log2f(sum)) * kLn2;
+        } else {
+          const int64_t at_row = ((int64_t)slot * p.c.H + kvh) * plan.part_rows + r;
+          float4* at = reinterpret_cast<float4*>(plan.part_o + at_row * D + 8 * ch);
+          at[0] = make_float4(x[0], x[1], x[2], x[3]);
+          at[1] = make_float4(x[4], x[5], x[6], x[7]);
+          if (ch == 0) plan.part_ml[at_row] = make_float2(m, sum);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        l[mt] += __shfl_xor(l[mt], 16, 64);
+        l[mt] += __shfl_xor(l[mt], 32, 64);
+        const int r = 16 * mt + n;
+        if (r >= rows) continue;
+        if (whole_seq) {
+          const int i = r / p.g, h = kvh * p.g + (r - i * p.g);
+          const float inv = l[mt] == 0.0f ? 0.0f : v_st / l[mt];
+          uint16_t* out = p.out + (s.row0 + i) * p.out_ld_t + h * p.out_ld_h + 4 * q * kTiles;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint32_t w[kTiles / 2];
+#pragma unroll
+            for (int j = 0; j < kTiles / 2; ++j)
+              w[j] = f32_to_bf16_any(o[mt][2 * j][v] * inv) | (f32_to_bf16_any(o[mt][2 * j + 1][v] * inv) << 16);
+            __builtin_memcpy(__builtin_assume_aligned(out + v * kTiles, kTiles < 8 ? 8 : 16), w, sizeof(w));
+          }
+          if (p.lse && q == 0)
+            p.lse[(int64_t)(s.row0 + i) * p.Hq + h] =
+                l[mt] == 0.0f ? -INFINITY : (ref[mt] + __builtin_log2f(l[mt])) * kLn2;
+        } else {
+          const int64_t at_row = ((int64_t)slot * p.c.H + kvh) * plan.part_rows + r;
+          float* at = plan.part_o + at_row * D + 4 * q * kTiles;
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int i = 0; i < kTiles; i += 4)
+              *reinterpret_cast<float4*>(at + v * kTiles + i) =
+                  make_float4(o[mt][i][v], o[mt][i + 1][v], o[mt][i + 2][v], o[mt][i + 3][v]);
+          if (q == 0) plan.part_ml[at_row] = make_float2(ref[mt], l[mt]);
+        }
       }
     }
   }
@@ -494,8 +541,11 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
 
 template <int D, int MT>
 int launch_rows(const AttnParams& p, const RowsPlan& plan, const ChunkPlan& chunk, hipStream_t s) {
-  hipLaunchKernelGGL((k_attn_rows<D, MT>), dim3((unsigned)(plan.workers * p.c.H + 1 + plan.plans_chunks)), dim3(256), 0,
-                     s, p, plan, chunk);
+  const dim3 grid((unsigned)(plan.workers * plan.waves / 4 * p.c.H + 1 + plan.plans_chunks));
+  if (plan.waves == 4)
+    hipLaunchKernelGGL((k_attn_rows<D, MT, 4>), grid, dim3(256), 0, s, p, plan, chunk);
+  else
+    hipLaunchKernelGGL((k_attn_rows<D, MT, 1>), grid, dim3(256), 0, s, p, plan, chunk);
   return last_launch();
 }
 
@@ -510,14 +560,22 @@ int attn_rows_tiles(int D, int64_t rows) {
 void attn_rows_plan(const AttnParams& p, int tiles, bool chunks, WsCarve& ws, RowsPlan& plan) {
   plan.plans_chunks = chunks;
   plan.max_rows = 16 * tiles;
-  const int64_t units = (p.num_keys + kUnit - 1) / kUnit + 1;  // most of a sequence
+  const int64_t units = (p.num_keys + unit_keys(4) - 1) / unit_keys(4) + 1;  // most of a sequence
   const int64_t places = (int64_t)rows_wgs_per_cu(p.c.D, tiles) * device_cu_count();
   plan.workers = 1;
   if (units * p.B > kFewUnits)
     plan.workers = (int)std::max<int64_t>(1, std::min((places - 1 - chunks) / p.c.H, units * p.B / kMinUnits));
+  // Waves as workers from a sequence for two workgroups on, if each of these
+  // would have eight units (head dimension 128, 32 heads on 8: 1024 sequences of
+  // up to 512 keys 109 us against 134, 256 of 1024 53 against 57, 64 of 8192 74
+  // against 75; 16 of 4000 22 against 21, 50 of 600 22 against 19).
+  const bool many = plan.workers > 1 && plan.workers <= 2 * p.B && units * p.B >= 8 * plan.workers;
+  plan.waves = many && p.B * (p.num_keys / 32 + 2) <= INT32_MAX ? 1 : 4;
+  plan.workers *= 4 / plan.waves;
+  plan.part_rows = (int)std::min<int64_t>(plan.max_rows, ((int64_t)p.max_q * p.g + 3) / 4 * 4);  // joined by fours
   plan.may_split = plan.workers > 1;
   plan.seq = ws.take<int32_t>(2 * (size_t)p.B);
-  const size_t rows = plan.may_split ? (size_t)(2 * plan.workers * p.c.H) * plan.max_rows : 0;
+  const size_t rows = plan.may_split ? (size_t)(2 * plan.workers * p.c.H) * plan.part_rows : 0;
   plan.part_ml = ws.take<float2>(rows);
   plan.part_o = ws.take<float>(rows * p.c.D);
 }

@@ -29,12 +29,14 @@ struct AttnParams {
 // Plan of the few-rows kernel, and where the parts of split sequences go.
 struct RowsPlan {
   int max_rows;  // sequences with more rows per key/value head are left out
-  int workers;   // most workgroups per key/value head
+  int workers;   // most of them per key/value head
+  int waves;     // of a worker: 4, or 1 (four workers a workgroup)
   int may_split;
+  int part_rows;  // rows of a part
   int plans_chunks;  // the launch has a workgroup that plans the many-rows one
   int32_t* seq;     // [B][2]: first worker and its slot (2 worker + slot), number of workers
-  float2* part_ml;  // [worker][2 slots][head][max_rows] reference and sum
-  float* part_o;    // [worker][2 slots][head][max_rows][D]
+  float2* part_ml;  // [worker][2 slots][head][part_rows] reference and sum
+  float* part_o;    // [worker][2 slots][head][part_rows][D]
 };
 
 int attn_rows_tiles(int D, int64_t rows);

@@ -412,13 +412,19 @@ def test_many_rows_divided_or_whole(D, seqs):
         _run(pages, seqs, Hq, window=130)
 
 
-@pytest.mark.parametrize("B,D,new", [(70, 128, 1), (300, 64, 2), (1100, 64, 1)])
-def test_many_sequences(B, D, new):
+@pytest.mark.parametrize("B,D,new,Hq,Hkv,far", [
+    (70, 128, 1, 2, 1, 150), (300, 64, 2, 2, 1, 150), (1100, 64, 1, 2, 1, 150), (64, 128, 1, 32, 8, 1500),
+    (200, 128, 2, 16, 16, 600), (100, 128, 5, 32, 8, 800), (90, 256, 2, 16, 8, 700), (100, 256, 9, 16, 8, 700),
+    (120, 64, 5, 32, 16, 500), (100, 64, 20, 32, 16, 500), (70, 128, 16, 32, 8, 800)])
+def test_many_sequences(B, D, new, Hq, Hkv, far):
     """More sequences than one step of the planning scans holds, empty ones among them."""
-    log(f"[attention] {B} sequences D={D}")
-    seqs = [(0 if i % 7 == 3 else new, (i * 37) % 150 + new) for i in range(B)]
-    pages = ref.Pages([b for _, b in seqs], 1, 16, D, seed=B)
-    _run(pages, seqs, 2)
+    log(f"[attention] {B} sequences D={D} {new} new tokens, heads {Hq}/{Hkv}")
+    seqs = [(0 if i % 7 == 3 else new, (i * 37) % far + new) for i in range(B)]
+    pages = ref.Pages([b for _, b in seqs], Hkv, 16, D, seed=B)
+    _run(pages, seqs, Hq)
+    _run(pages, seqs, Hq, window=33)
+    if Hq > 2:
+        return
     some = [(40 if i % 97 == 5 else n, max(b, 40)) for i, (n, b) in enumerate(seqs)]
     _run(ref.Pages([b for _, b in some], 1, 16, D, seed=B + 1), some, 2)
 
