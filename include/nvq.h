@@ -559,7 +559,8 @@ typedef struct nvq_paged_attention_args {
 } nvq_paged_attention_args;
 
 /* Workspace of a call with these arguments (only the sizes are read: total_q,
- * B, max_q, q_heads, table_width and the cache's heads, head_dim, page_size). */
+ * B, max_q, q_heads, window, table_width and the cache's heads, head_dim,
+ * page_size). */
 size_t nvq_paged_attention_workspace_bytes(const nvq_kv_cache* cache,
                                            const nvq_paged_attention_args* args);
 /* Limits: total_q < 2^24, q_heads <= 32768, total_q * q_heads <= 2^30, B <=

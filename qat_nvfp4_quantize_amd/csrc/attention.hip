@@ -162,6 +162,7 @@ int attn_sizes(const nvq_kv_cache* cache, const nvq_paged_attention_args* a, Att
   p.max_q = (int)(a->max_q == 0 ? a->total_q : std::min(a->max_q, a->total_q));
   p.Hq = a->q_heads, p.g = a->q_heads / cache->heads;
   p.num_keys = a->table_width * ps;
+  p.window = std::min<int64_t>(a->window, INT32_MAX);  // past every key; sums with it stay in range
   p.c.H = cache->heads, p.c.D = cache->head_dim;
   return NVQ_OK;
 }
@@ -240,7 +241,6 @@ extern "C" int nvq_paged_attention(const nvq_kv_cache* cache, const nvq_paged_at
   if (!a.q || !a.out || !a.cu_q || !a.kv_len || (!a.block_table && a.table_width > 0)) return NVQ_EINVAL;
   p.q = a.q, p.out = a.out, p.lse = a.lse;
   p.cu_q = a.cu_q, p.kv_len = a.kv_len, p.table = a.block_table;
-  p.window = std::min<int64_t>(a.window, INT32_MAX);  // past every key; sums with it stay in range
   p.causal = a.causal;
   p.scale_log2 = a.softmax_scale * kLog2e;
   if (plan.use_rows || plan.use_chunk) {

@@ -3,8 +3,8 @@
 // dequantized once for 128 or 256 rows.
 //
 // A workgroup takes 128 (token, head-of-the-group) rows of one sequence and
-// key/value head (256 at head dimension 128), a wave 32 of them, over 64 keys
-// at a time.  The keys' codes
+// key/value head (256 at head dimension 128 and many keys), a wave 32 of them,
+// over 64 keys at a time.  The keys' codes
 // come into registers one tile ahead, are dequantized exactly to fp16 and
 // written row-major to LDS (K and V alike, double-buffered, one barrier a
 // tile).  Products run transposed (32x32x16 fp16): S^T = K Q^T leaves a lane
@@ -439,9 +439,16 @@ __global__ __launch_bounds__(1024) void k_attn_chunk_plan(AttnParams p, ChunkPla
 void attn_chunk_plan(const AttnParams& p, int min_rows, bool check, WsCarve& ws, ChunkPlan& plan) {
   plan.min_rows = min_rows;
   plan.check = check;
-  // rows of a sequence are cut to the call's, so its tiles are at most this
-  const int waves = p.c.D == 128 && (int64_t)p.max_q * p.g > 128 ? 8 : 4;
+  // Head dimension 128: 256-row tiles halve the dequantization of a row, but
+  // only one workgroup fits a CU, so nothing covers the start and the end of a
+  // tile; two with 128 rows where rows see few keys.  32 heads on 8: chunks of
+  // 1024 and 1536 new tokens 71 us against 81 and 93 against 107, windows of 512
+  // and 1024 129 against 147 and 192 against 203; two chunks of 2048 96 against
+  // 104, 4096 behind 4096 713 against 741.
+  const bool far = p.window > 0 ? std::min(p.window, p.num_keys) > 1024 : p.num_keys >= 2048;
+  const int waves = p.c.D == 128 && (int64_t)p.max_q * p.g > 128 && far ? 8 : 4;
   plan.tile_rows = 32 * waves;
+  // rows of a sequence are cut to the call's, so its tiles are at most this
   plan.max_tiles = (int64_t)p.total_q * p.g / plan.tile_rows + p.B;
   const int64_t units = (p.num_keys + kTileKeys - 1) / kTileKeys + 1;  // most of a tile
   const int64_t places = (int64_t)chunk_wgs_per_cu(p.c.D, waves) * device_cu_count() - plan.check;

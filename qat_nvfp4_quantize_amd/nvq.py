@@ -6,7 +6,6 @@ the library is missing or the device is not a GPU, calls raise.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import struct
@@ -529,7 +528,6 @@ def qat_fakequant_gemm_w4a16(mode, w_codes, w_scales, w_tensor_scale, expert_off
 _HEAD_TYPES = (torch.bfloat16, torch.float32)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-_HERE = contextlib.nullcontext()
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
@@ -732,8 +730,12 @@ def nvq_paged_attention(q, cache, cu_q, kv_len, block_table, max_q=None, scale=N
             0 if lse is None else lse.data_ptr())
     L = _lib or load()
     if ws is None:
-        with torch.cuda.device(dev) if _current_device() != dev.index else _HERE:
-            nbytes = L.nvq_paged_attention_workspace_bytes(cache._ref, _ATTENTION.pack(*head, 0, 0))
+        args = _ATTENTION.pack(*head, 0, 0)
+        if _current_device() == dev.index:
+            nbytes = L.nvq_paged_attention_workspace_bytes(cache._ref, args)
+        else:
+            with torch.cuda.device(dev):
+                nbytes = L.nvq_paged_attention_workspace_bytes(cache._ref, args)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _call(L.nvq_paged_attention, "nvq_paged_attention", dev, cache._ref,
           _ATTENTION.pack(*head, ws.data_ptr(), ws.numel()))

@@ -63,6 +63,13 @@ def _run(pages, seqs, Hq, causal=True, window=0, seed=1, gap=3, max_q="max", qs=
     return out, lse
 
 
+def _wide(pages, keys=2048):
+    """The same pages under a block table that covers at least so many keys."""
+    pages.table = np.pad(pages.table, ((0, 0), (0, max(0, -(-keys // pages.S) - pages.width))), constant_values=-7)
+    pages.width = pages.table.shape[1]
+    return pages
+
+
 # (new, length) of each sequence
 DECODE = [(1, 1), (1, 37), (1, 640), (1, 16), (0, 50), (1, 129), (0, 0), (1, 300)]
 DRAFTS = [(4, 4), (3, 200), (4, 65), (1, 33), (0, 9), (4, 517)]
@@ -401,6 +408,7 @@ def test_rows_of_every_kernel_variant(D, Hq, Hkv, n):
     [(300, 300), (70, 1500)],              # several row tiles of 128 or 256
     [(40, 40 + 17 * i) for i in range(9)] + [(1, 600), (150, 150)],
     [(33, 5000), (200, 260)],              # few row tiles: their keys divided
+    [(300, 2300), (90, 2100), (1, 70), (257, 257), (0, 9)],
     [(64, 64)] * 60,                       # many: handed out whole
 ])
 def test_many_rows_divided_or_whole(D, seqs):
@@ -410,6 +418,10 @@ def test_many_rows_divided_or_whole(D, seqs):
     _run(pages, seqs, Hq)
     if len(seqs) < 20:
         _run(pages, seqs, Hq, window=130)
+    if D == 128:  # 256-row tiles
+        _run(_wide(pages), seqs, Hq)
+        if len(seqs) < 20:
+            _run(pages, seqs, Hq, window=1100)
 
 
 @pytest.mark.parametrize("B,D,new,Hq,Hkv,far", [
@@ -460,8 +472,8 @@ def test_moving_reference(D, n, Hq, order):
     seqs = [(n, length), (n, length)]
     q, cu, lens = _batch(seqs, Hq, D, 5)
     q = q.abs()
-    args = [torch.from_numpy(x).cuda() for x in (cu, lens, pages.table)]
-    for scale in (2.0, 30.0):
+    for scale, keys in ((2.0, 0), (30.0, 0), (2.0, 2048), (30.0, 2048)):
+        args = [torch.from_numpy(x).cuda() for x in (cu, lens, _wide(pages, keys).table)]
         out = nvq.nvq_paged_attention(q.cuda(), pages.cache(nvq), *args, max_q=n, scale=scale)
         out = out.float().cpu().numpy().astype(np.float64)
         qn = q.float().numpy().astype(np.float64)
@@ -493,9 +505,9 @@ def test_row_ranges_that_overlap_stay_in_bounds():
     nvq = _nvq()
     n = 200
     seqs = [(n, 300)] * 5
-    for D, Hq in ((128, 4), (64, 2), (256, 2), (48, 2)):
-        log(f"[attention] overlapping rows D={D}")
-        pages = ref.Pages([300] * 5, 1, 16, D, seed=D)
+    for D, Hq, keys in ((128, 4, 0), (128, 4, 2048), (64, 2, 0), (256, 2, 0), (48, 2, 0)):
+        log(f"[attention] overlapping rows D={D}, table of {keys}")
+        pages = _wide(ref.Pages([300] * 5, 1, 16, D, seed=D), keys)
         q = torch.randn(2 * n, Hq, D, device="cuda").to(torch.bfloat16)
         cache = pages.cache(nvq)
         lens = torch.full((5,), 300, dtype=torch.int32, device="cuda")
