@@ -12,10 +12,13 @@ namespace nvq {
 
 constexpr int kTileKeys = 64;
 constexpr int kChunkMinUnits = 4;  // key tiles of a run, where there are so many
-// With this many row tiles per place they go out whole, the ones with most
-// keys first; with fewer the units are dealt in equal runs, which costs a
-// second pass over the divided tiles.
-constexpr float kWholeTiles = 1.5f;
+// Row tiles go out whole, those with most keys first, or their units are dealt
+// in equal runs, which costs about 20 units' time for the divided tiles' parts
+// (written once and read by the join) where all places take part.  With this
+// many tiles per place they go out whole in any case; with fewer, whichever is
+// expected to take less: 1000 new tokens, 32 heads on 8 of 128, 39 us whole
+// against 71, 512 behind 7488 105 divided (a fourth of the places whole).
+constexpr float kWholeTiles = 1.5f, kJoinUnits = 20;
 
 // Keys of row tile qt of sequence s, in 64-key tiles from `base`.
 struct TileRange {
@@ -52,15 +55,19 @@ __device__ __forceinline__ void plan_chunks(const AttnParams& p, const ChunkPlan
     __syncthreads();
     return lds.last;
   };
+  // numbers up to `most`: their sum over the workgroup fits 32 bits, or takes two scans
+  auto scan = [&](int v, int64_t most) -> int64_t {
+    return most * threads <= INT32_MAX ? block_inclusive_scan(v, lds.scan) : block_inclusive_scan_wide(v, lds.scan);
+  };
   int tiles = 0;
   for (int b0 = 0; b0 < p.B; b0 += threads) {
     int n = 0;
     if (b0 + t < p.B) {
       const Seq s = load_seq(p, b0 + t);
       const int64_t rows = (int64_t)s.n * p.g;
-      n = rows > plan.min_rows ? (int)((rows + plan.tile_rows - 1) / plan.tile_rows) : 0;
+      n = rows > plan.min_rows ? (int)min<int64_t>((rows + plan.tile_rows - 1) / plan.tile_rows, plan.max_tiles) : 0;
     }
-    const int64_t incl = tiles + block_inclusive_scan_wide(n, lds.scan);
+    const int64_t incl = tiles + scan(n, plan.max_tiles);
     const int end = (int)min<int64_t>(incl, plan.max_tiles);
     if (b0 + t < 1024) lds.end[b0 + t] = end;
     if (b0 + t < p.B) plan.tile_end[b0 + t] = end;
@@ -70,6 +77,7 @@ __device__ __forceinline__ void plan_chunks(const AttnParams& p, const ChunkPlan
   __syncthreads();
   auto end_of = [&](int b) { return b < 1024 ? lds.end[b] : plan.tile_end[b]; };
   int64_t total = 0;
+  int most = 0;
   for (int i0 = 0; i0 < tiles; i0 += threads) {
     const int i = i0 + t;
     int units = 0;
@@ -86,12 +94,22 @@ __device__ __forceinline__ void plan_chunks(const AttnParams& p, const ChunkPlan
       units = tile_range(p, load_seq(p, lo), qt, plan.tile_rows).units;
       plan.tile[i] = make_int2(lo, qt);
     }
-    const int64_t incl = total + block_inclusive_scan_wide(units, lds.scan);
+    const int64_t incl = total + scan(units, p.num_keys / kTileKeys + 2);
+    most = max(most, units);
     if (i < tiles) plan.unit_end[i] = incl;
     total = last(incl);
   }
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) most = max(most, __shfl_xor(most, off, 64));
+  if ((t & 63) == 0) lds.scan[t >> 6] = most;
+  __syncthreads();
+  for (int i = 0; i < threads / 64; ++i) most = max(most, lds.scan[i]);
   const int64_t workers = max<int64_t>(1, min<int64_t>(plan.workers, total / kChunkMinUnits));
-  const bool divide = (float)tiles < kWholeTiles * (float)workers && workers > 1;
+  const float runs = (float)workers, places = (float)plan.workers;
+  float whole = (float)most;  // units that a place takes in turn, expected
+  if ((float)tiles > places) whole = fmaxf(whole, 1.8f * (float)total / (float)tiles);
+  const bool divide = workers > 1 && (float)tiles < kWholeTiles * places &&
+                      (float)total / runs + kJoinUnits * runs / places < whole;
   if (t == 0) {
     plan.info[0] = divide ? workers : tiles;
     plan.info[1] = divide;
