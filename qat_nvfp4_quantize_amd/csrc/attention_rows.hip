@@ -87,11 +87,12 @@ __device__ __forceinline__ int chunk_units(const AttnParams& p, int max_rows, in
   return wave_inclusive_scan(units);
 }
 
-// Units of a workgroup's run, where there are so many; and units of the whole
-// call up to which one workgroup a head takes them all, which spares the
-// joining launch (one sequence of 777 keys: 13.1 us against 15.4, of 1024: 14.2
-// against 15.4, of 1500: 17.7 against 14.8).
-constexpr int kMinUnits = 2, kFewUnits = 10;
+// Units of a workgroup's run, where there are so many; and most units of a
+// sequence that takes one workgroup a head whole, which spares the joining
+// launch (one of 777 keys: 13.1 us against 15.4, of 1024: 14.2 against 15.4, of
+// 1500: 17.7 against 14.8; 60 of up to 900: 16.6 against 21.1, 24 of up to 459:
+// 11.6 against 14.9).
+constexpr int kMinUnits = 2, kFewUnits = 9;
 
 // Workgroups of a kernel variant that a CU holds (its register budget).
 constexpr int rows_wgs_per_cu(int D, int MT) {
@@ -208,12 +209,21 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
   const int worker = W == 4 ? block / p.c.H : block / p.c.H * 4 + wave, share = W == 4 ? wave : 0;  // share of a unit
 
   // this worker's run [x, x_end) of the units of all sequences
-  int chunk = 0, incl = chunk_units<W>(p, plan.max_rows, 0), total = __builtin_amdgcn_readlane(incl, 63);
-  for (int c = 1; 64 * c < p.B; ++c) total += __builtin_amdgcn_readlane(chunk_units<W>(p, plan.max_rows, c), 63);
-  const int workers = min(plan.workers, max(1, total / (kMinUnits * 4 / W)));
-  if (worker >= workers || total == 0) return;
-  int x = (int)((int64_t)worker * total / workers);
-  const int x_begin = x, x_end = (int)((int64_t)(worker + 1) * total / workers);
+  int chunk = W == 4 && plan.whole ? worker >> 6 : 0;
+  int incl = chunk_units<W>(p, plan.max_rows, chunk), total = __builtin_amdgcn_readlane(incl, 63), workers = 1;
+  int x, x_end;
+  if (W == 4 && plan.whole) {  // a sequence
+    x = (worker & 63) ? __builtin_amdgcn_readlane(incl, (worker & 63) - 1) : 0;
+    x_end = __builtin_amdgcn_readlane(incl, worker & 63);
+  } else {
+    for (int c = 1; 64 * c < p.B; ++c) total += __builtin_amdgcn_readlane(chunk_units<W>(p, plan.max_rows, c), 63);
+    workers = min(plan.workers, max(1, total / (kMinUnits * 4 / W)));
+    if (worker >= workers) return;
+    x = (int)((int64_t)worker * total / workers);
+    x_end = (int)((int64_t)(worker + 1) * total / workers);
+  }
+  if (x == x_end) return;
+  const int x_begin = x;
   int before = 0;  // units of earlier chunks
   const float c0 = p.scale_log2 * *p.c.k_st, v_st = *p.c.v_st;
 
@@ -242,7 +252,7 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
     // inside a sequence begun within the run to slot 1
     const bool whole_seq = u_begin == 0 && u_end == range.units;
     const int slot = x == x_begin ? 2 * worker : 2 * worker + 1;
-    if (u_begin == 0 && kvh == 0 && (W == 4 ? threadIdx.x : threadIdx.x & 63) == 0) {
+    if (plan.may_split && u_begin == 0 && kvh == 0 && (W == 4 ? threadIdx.x : threadIdx.x & 63) == 0) {
       const int last = (int)(((int64_t)(seq_x + range.units) * workers - 1) / total);
       plan.seq[2 * b] = slot;
       plan.seq[2 * b + 1] = last - worker + 1;
@@ -560,20 +570,22 @@ int attn_rows_tiles(int D, int64_t rows) {
 void attn_rows_plan(const AttnParams& p, int tiles, bool chunks, WsCarve& ws, RowsPlan& plan) {
   plan.plans_chunks = chunks;
   plan.max_rows = 16 * tiles;
-  const int64_t units = (p.num_keys + unit_keys(4) - 1) / unit_keys(4) + 1;  // most of a sequence
+  // most keys of a sequence, from a multiple of 32 on, and units
+  const int64_t keys = p.window > 0 ? std::min(p.num_keys, p.window + p.max_q + 30) : p.num_keys;
+  const int64_t units = std::max<int64_t>(1, (keys + unit_keys(4) - 1) / unit_keys(4));
   const int64_t places = (int64_t)rows_wgs_per_cu(p.c.D, tiles) * device_cu_count();
-  plan.workers = 1;
-  if (units * p.B > kFewUnits)
-    plan.workers = (int)std::max<int64_t>(1, std::min((places - 1 - chunks) / p.c.H, units * p.B / kMinUnits));
+  plan.workers = (int)std::max<int64_t>(1, std::min((places - 1 - chunks) / p.c.H, units * p.B / kMinUnits));
   // Waves as workers from a sequence for two workgroups on, if each of these
   // would have eight units (head dimension 128, 32 heads on 8: 1024 sequences of
   // up to 512 keys 109 us against 134, 256 of 1024 53 against 57, 64 of 8192 74
   // against 75; 16 of 4000 22 against 21, 50 of 600 22 against 19).
-  const bool many = plan.workers > 1 && plan.workers <= 2 * p.B && units * p.B >= 8 * plan.workers;
-  plan.waves = many && p.B * (p.num_keys / 32 + 2) <= INT32_MAX ? 1 : 4;
-  plan.workers *= 4 / plan.waves;
+  const bool many = plan.workers > 1 && plan.workers <= 2 * p.B && units * p.B >= 8 * plan.workers &&
+                    p.B * (p.num_keys / 32 + 2) <= INT32_MAX;
+  plan.waves = many ? 1 : 4;
+  plan.whole = !many && units <= kFewUnits;
+  plan.workers = plan.whole ? (int)p.B : plan.workers * (4 / plan.waves);
+  plan.may_split = !plan.whole && plan.workers > 1;
   plan.part_rows = (int)std::min<int64_t>(plan.max_rows, ((int64_t)p.max_q * p.g + 3) / 4 * 4);  // joined by fours
-  plan.may_split = plan.workers > 1;
   plan.seq = ws.take<int32_t>(2 * (size_t)p.B);
   const size_t rows = plan.may_split ? (size_t)(2 * plan.workers * p.c.H) * plan.part_rows : 0;
   plan.part_ml = ws.take<float2>(rows);

@@ -31,6 +31,7 @@ struct RowsPlan {
   int max_rows;  // sequences with more rows per key/value head are left out
   int workers;   // most of them per key/value head
   int waves;     // of a worker: 4, or 1 (four workers a workgroup)
+  int whole;     // a worker is a sequence
   int may_split;
   int part_rows;  // rows of a part
   int plans_chunks;  // the launch has a workgroup that plans the many-rows one
