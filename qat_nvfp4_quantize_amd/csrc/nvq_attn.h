@@ -49,7 +49,8 @@ void attn_rows_plan(const AttnParams& p, int tiles, bool chunks, WsCarve& ws, Ro
 struct ChunkPlan {
   int min_rows;  // sequences with no more rows per key/value head are left out
   int check;     // the launch checks the index arrays
-  int workers;   // runs per key/value head where tiles are divided
+  int places;    // workgroups that the chip holds, per key/value head
+  int workers;   // most runs per key/value head where tiles are divided
   int tile_rows;  // 128 or 256
   int64_t max_tiles;
   int32_t* tile_end;   // [B] row tiles up to and with sequence b

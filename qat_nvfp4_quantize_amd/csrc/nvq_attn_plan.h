@@ -11,14 +11,14 @@
 namespace nvq {
 
 constexpr int kTileKeys = 64;
-constexpr int kChunkMinUnits = 4;  // key tiles of a run, where there are so many
+constexpr int kChunkMinUnits = 2;  // key tiles of a run, at least
 // Row tiles go out whole, those with most keys first, or their units are dealt
-// in equal runs, which costs about 20 units' time for the divided tiles' parts
-// (written once and read by the join) where all places take part.  With this
-// many tiles per place they go out whole in any case; with fewer, whichever is
-// expected to take less: 1000 new tokens, 32 heads on 8 of 128, 39 us whole
-// against 71, 512 behind 7488 105 divided (a fourth of the places whole).
-constexpr float kWholeTiles = 1.5f, kJoinUnits = 20;
+// in equal runs, whose divided tiles leave parts that the join reads: about 4
+// units' time, and 16 more if all places take part.  With this many tiles per
+// place they go out whole in any case; with fewer, whichever is expected to take
+// less: 1000 new tokens, 32 heads on 8 of 128, 39 us whole against 71; 79 behind
+// 1116 of one head of 256 31 us divided against 60.
+constexpr float kWholeTiles = 1.5f, kJoinUnits = 4, kPartUnits = 16;
 
 // Keys of row tile qt of sequence s, in 64-key tiles from `base`.
 struct TileRange {
@@ -104,12 +104,12 @@ __device__ __forceinline__ void plan_chunks(const AttnParams& p, const ChunkPlan
   if ((t & 63) == 0) lds.scan[t >> 6] = most;
   __syncthreads();
   for (int i = 0; i < threads / 64; ++i) most = max(most, lds.scan[i]);
+  const float places = (float)plan.places, units = (float)total;
   const int64_t workers = max<int64_t>(1, min<int64_t>(plan.workers, total / kChunkMinUnits));
-  const float runs = (float)workers, places = (float)plan.workers;
   float whole = (float)most;  // units that a place takes in turn, expected
-  if ((float)tiles > places) whole = fmaxf(whole, 1.8f * (float)total / (float)tiles);
+  if ((float)tiles > places) whole = fmaxf(whole, 1.8f * units / (float)tiles);
   const bool divide = workers > 1 && (float)tiles < kWholeTiles * places &&
-                      (float)total / runs + kJoinUnits * runs / places < whole;
+                      units / (float)workers + kJoinUnits + kPartUnits * (float)workers / places < whole;
   if (t == 0) {
     plan.info[0] = divide ? workers : tiles;
     plan.info[1] = divide;
