@@ -31,7 +31,7 @@
 // with pieces cut per sequence 64 ragged sequences made 1232 pieces for 768
 // places, two rounds of 33 us.
 //
-// Measured: 64 sequences of up to 8192 keys, 32 heads on 8 of 128: 73 us (a
+// Measured: 64 sequences of up to 8192 keys, 32 heads on 8 of 128: 72 us (a
 // copy moves the same bytes in 63), of which the loop takes 57 at 5.6 TB/s, the
 // rest goes to finding the runs, the first loads and the join; one sequence of
 // 131072 keys, 64 heads on 8: 43 us (30).
