@@ -451,7 +451,8 @@ void attn_chunk_plan(const AttnParams& p, int min_rows, bool check, WsCarve& ws,
   // rows of a sequence are cut to the call's, so its tiles are at most this
   plan.max_tiles = (int64_t)p.total_q * p.g / plan.tile_rows + p.B;
   const int64_t units = (p.num_keys + kTileKeys - 1) / kTileKeys + 1;  // most of a tile
-  const int64_t places = (int64_t)chunk_wgs_per_cu(p.c.D, waves) * device_cu_count() - plan.check;
+  plan.per_cu = chunk_wgs_per_cu(p.c.D, waves);
+  const int64_t places = (int64_t)plan.per_cu * device_cu_count() - plan.check;
   plan.places = (int)std::max<int64_t>(1, places / p.c.H);
   plan.workers = (int)std::max<int64_t>(1, std::min<int64_t>(plan.places, units * plan.max_tiles / kChunkMinUnits));
   plan.info = ws.take<int64_t>(3);

@@ -50,6 +50,7 @@ struct ChunkPlan {
   int min_rows;  // sequences with no more rows per key/value head are left out
   int check;     // the launch checks the index arrays
   int places;    // workgroups that the chip holds, per key/value head
+  int per_cu;    // and per CU
   int workers;   // most runs per key/value head where tiles are divided
   int tile_rows;  // 128 or 256
   int64_t max_tiles;

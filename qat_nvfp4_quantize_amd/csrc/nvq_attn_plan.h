@@ -17,8 +17,10 @@ constexpr int kChunkMinUnits = 2;  // key tiles of a run, at least
 // units' time, and 16 more if all places take part.  With this many tiles per
 // place they go out whole in any case; with fewer, whichever is expected to take
 // less: 1000 new tokens, 32 heads on 8 of 128, 39 us whole against 71; 79 behind
-// 1116 of one head of 256 31 us divided against 60.
-constexpr float kWholeTiles = 1.5f, kJoinUnits = 4, kPartUnits = 16;
+// 1116 of one head of 256 31 us divided against 60.  A workgroup alone on a CU
+// that holds more takes kLonePace of a unit's time (1523 new tokens, 16 heads on
+// 4 of 64: 46 us whole against 68).
+constexpr float kWholeTiles = 1.5f, kJoinUnits = 4, kPartUnits = 16, kLonePace = 0.6f;
 
 // Keys of row tile qt of sequence s, in 64-key tiles from `base`.
 struct TileRange {
@@ -106,10 +108,15 @@ __device__ __forceinline__ void plan_chunks(const AttnParams& p, const ChunkPlan
   for (int i = 0; i < threads / 64; ++i) most = max(most, lds.scan[i]);
   const float places = (float)plan.places, units = (float)total;
   const int64_t workers = max<int64_t>(1, min<int64_t>(plan.workers, total / kChunkMinUnits));
+  // a unit's time with n workgroups at work, against that with all places taken
+  const float per_cu = (float)plan.per_cu;
+  auto pace = [&](float n) {
+    return per_cu == 1.0f ? 1.0f : fmaxf(kLonePace, fminf(1.0f, __builtin_ceilf(n * per_cu / places) / per_cu));
+  };
   float whole = (float)most;  // units that a place takes in turn, expected
   if ((float)tiles > places) whole = fmaxf(whole, 1.8f * units / (float)tiles);
-  const bool divide = workers > 1 && (float)tiles < kWholeTiles * places &&
-                      units / (float)workers + kJoinUnits + kPartUnits * (float)workers / places < whole;
+  const float runs = (float)workers, divided = units / runs * pace(runs) + kJoinUnits + kPartUnits * runs / places;
+  const bool divide = workers > 1 && (float)tiles < kWholeTiles * places && divided < whole * pace((float)tiles);
   if (t == 0) {
     plan.info[0] = divide ? workers : tiles;
     plan.info[1] = divide;
