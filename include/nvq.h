@@ -536,7 +536,8 @@ int nvq_kv_gather(const nvq_kv_cache* cache, const int32_t* slots, int64_t T, vo
  * such keys are left out, a negative length counts as 0, ranges are cut to
  * [0, total_q] and rows past the max_q-th are not written.  No call reads or
  * writes outside its buffers for any content of the index arrays.  Sequences
- * may share pages.  Calls on one stream may share a workspace. */
+ * may share pages.  out may be q with the same strides; it overlaps nothing else
+ * of the call.  Calls on one stream may share a workspace. */
 typedef struct nvq_paged_attention_args {
   size_t struct_size;          /* sizeof(nvq_paged_attention_args) */
   int64_t total_q, B;          /* query rows; sequences */

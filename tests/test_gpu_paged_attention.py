@@ -586,3 +586,18 @@ def test_equal_calls_give_equal_bits():
         first = nvq.nvq_paged_attention(*args, max_q=n)
         for _ in range(5):
             assert torch.equal(nvq.nvq_paged_attention(*args, max_q=n)[:cu[-1]], first[:cu[-1]])
+
+
+@pytest.mark.parametrize("D,seqs", [(128, [(1, 3000), (1, 40), (2, 77)]), (256, [(1, 9)] * 70), (64, [(200, 5000)]),
+                                    (128, [(300, 300), (1, 20), (70, 2500)]), (48, [(3, 50), (1, 9)])])
+def test_output_in_place_of_the_queries(D, seqs):
+    import torch
+
+    nvq = _nvq()
+    pages = ref.Pages([b for _, b in seqs], 2, 16, D, seed=D)
+    q, cu, lens = _batch(seqs, 8, D, 4)
+    q, args = q.cuda(), [pages.cache(nvq)] + [torch.from_numpy(x).cuda() for x in (cu, lens, pages.table)]
+    n = max(a for a, _ in seqs)
+    want = nvq.nvq_paged_attention(q, *args, max_q=n)
+    got = nvq.nvq_paged_attention(q, *args, max_q=n, out=q)
+    assert got is q and torch.equal(got, want)
