@@ -481,10 +481,10 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
         const int r = e / kChunks, ch = e - r * kChunks;
         if (r >= rows) break;
         const float m = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
-        float sum = 0.0f;
+        float sum = 0.0f;  // a wave whose scores are all NaN has no reference either, but a sum of NaN: it counts
 #pragma unroll
         for (int w = 0; w < 4; ++w)
-          sum += s_m[w][r] == -INFINITY ? 0.0f : s_l[w][r] * __builtin_amdgcn_exp2f(s_m[w][r] - m);
+          sum += s_l[w][r] * (s_m[w][r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(s_m[w][r] - m));
         float x[8];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
