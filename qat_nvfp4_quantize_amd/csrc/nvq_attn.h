@@ -99,21 +99,24 @@ __device__ __forceinline__ void visible(const AttnParams& p, const Seq& s, int64
 // stay inside the buffers, so no atomic and no clearing is needed.  A batch
 // of 256 sequences at a time, a thread each, then the pages of all of them in
 // one run, so that few loads wait for one another (64 sequences of 64 pages:
-// 17 us with a loop over the sequences, hidden now).
+// 17 us with a loop over the sequences, hidden now).  Every thread of the
+// workgroup calls it, 256 or more: those past the batch add nothing to the scan.
+constexpr int kCheckBatch = 256;
 struct CheckLds {
-  int end[256];  // pages of the batch's sequences up to and with this one
-  int first[256];
+  int end[kCheckBatch];  // pages of the batch's sequences up to and with this one
+  int first[kCheckBatch];
   int wave[16];
   uint32_t flag;
 };
 __device__ __forceinline__ void check_batch(const AttnParams& p, CheckLds& lds) {
-  const int t = threadIdx.x;  // of 256
+  const int t = threadIdx.x;
+  const bool in_batch = t < kCheckBatch;
   if (t == 0) lds.flag = 0u;
   bool bad = false;
-  for (int b0 = 0; b0 < p.B; b0 += 256) {
+  for (int b0 = 0; b0 < p.B; b0 += kCheckBatch) {
     const int b = b0 + t;
     int first = 0, n = 0;
-    if (b < p.B) {
+    if (in_batch && b < p.B) {
       const int64_t r0 = p.cu_q[b], r1 = p.cu_q[b + 1], len = p.kv_len[b];
       bad |= r0 < 0 || r1 < r0 || r1 > p.total_q || r1 - r0 > p.max_q || len < 0 || (r1 > r0 && len > p.num_keys);
       const Seq s = load_seq(p, b);
@@ -128,14 +131,14 @@ __device__ __forceinline__ void check_batch(const AttnParams& p, CheckLds& lds) 
       }
     }
     __syncthreads();
-    lds.first[t] = first;
+    if (in_batch) lds.first[t] = first;
     const int incl = block_inclusive_scan(n, lds.wave);
-    lds.end[t] = incl;
+    if (in_batch) lds.end[t] = incl;
     __syncthreads();
-    const int all = lds.end[255];
+    const int all = lds.end[kCheckBatch - 1];
 #pragma unroll 4
-    for (int i = t; i < all; i += 256) {
-      int lo = 0, hi = 255;
+    for (int i = t; i < all; i += blockDim.x) {
+      int lo = 0, hi = kCheckBatch - 1;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (lds.end[mid] > i)

@@ -65,3 +65,117 @@ def test_log_sum_exp_of_a_query_that_is_not_finite(D, Hkv, seqs):
     same = torch.ones(q.shape[:2], dtype=torch.bool, device="cuda")
     same[0, 1] = same[-1, 0] = False
     assert torch.equal(out[same], clean[same]) and torch.equal(lse[same], clean_lse[same])
+
+
+def _compare(pages, seqs, q, cu, out, lse, scale, room=0.0):
+    """Every row of (out, lse) against 64 bits.  room: what the result's format
+    adds to the bound, where results are below its normal numbers."""
+    out, lse = (t.double().cpu().numpy() for t in (out, lse))
+    qn = q.double().numpy()
+    for b, (n, length) in enumerate(seqs):
+        k, v = pages.rows(b, length)
+        r = slice(cu[b], cu[b + 1])
+        want, wlse, tol = ref.attention(qn[r], k, v, length - n, scale, True, 0)
+        off = np.abs(out[r] - want)
+        assert (off <= tol + room).all(), (b, n, length, float((off - tol).max()), float(np.abs(want).max()))
+        # the score error and the sum's, a few roundings of lse itself
+        absum = np.abs(qn[r]).max(initial=0) * np.abs(k).sum(-1).max(initial=0) * abs(scale)
+        near = ref.U32 * (pages.D * absum + 2 * length + 64 + 16 * np.abs(wlse).max(initial=0))
+        assert (np.abs(lse[r] - wlse) <= near).all(), (b, n, length)
+
+
+def _table_of(pages, keys):
+    """Widens the block table to at least so many keys."""
+    more = max(0, -(-keys // pages.S) - pages.width)
+    pages.table = np.pad(pages.table, ((0, 0), (0, more)), constant_values=-7)
+    pages.width += more
+
+
+# Calls without a few-rows launch, whose many-rows launch looks the index arrays
+# over itself: one sequence, or more than 64 query heads a key/value head.
+# (D, query heads, key/value heads, sequences, keys of the table): the table's
+# width chooses 256-row tiles at head dimension 128
+ALONE = [(64, 8, 2, [(300, 900)], 0), (128, 8, 2, [(300, 900)], 0), (128, 8, 2, [(300, 900)], 2048),
+         (128, 4, 1, [(150, 2600)], 0), (256, 8, 2, [(150, 900)], 0), (128, 70, 1, [(3, 300), (0, 9), (2, 77)], 0),
+         (128, 70, 1, [(3, 300), (0, 9), (2, 77)], 2048), (256, 70, 1, [(3, 300), (2, 77)], 0)]
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,seqs,keys", ALONE)
+def test_many_rows_alone(D, Hq, Hkv, seqs, keys):
+    log(f"[attention] many rows alone D={D} heads={Hq}/{Hkv} {seqs} table of {keys}")
+    pages = ref.Pages([b for _, b in seqs], Hkv, 64, D, seed=D + len(seqs))
+    _table_of(pages, keys)
+    q, cu, lens = _queries(seqs, Hq, D, 7)
+    ws = _nvq().workspace(256 << 20, "cuda")
+    out, lse = _attend(pages, q, cu, lens, ws=ws)
+    assert _nvq().device_status(ws) == 0
+    _compare(pages, seqs, q, cu, out, lse, D ** -0.5)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,seqs,keys", ALONE)
+def test_many_rows_alone_report_bad_index_arrays(D, Hq, Hkv, seqs, keys):
+    import torch
+
+    nvq = _nvq()
+    log(f"[attention] bad index arrays, many rows alone D={D} heads={Hq}/{Hkv} {seqs} table of {keys}")
+    pages = ref.Pages([b for _, b in seqs], Hkv, 64, D, seed=D)
+    _table_of(pages, keys)
+    q, cu, lens = _queries(seqs, Hq, D, 7)
+    ws = nvq.workspace(256 << 20, "cuda")
+    cache, table, last = pages.cache(nvq), pages.table, len(seqs) - 1
+
+    def run(cu=cu, lens=lens, **more):
+        out, lse = _attend(pages, q, cu, lens, cache, ws, **more)
+        return out, lse, nvq.device_status(ws)
+
+    def others_hold(out, lse):
+        # Not bit by bit: one sequence's length moves the cuts through the others' keys, a part's reference is no
+        # whole power of two, and so the weights under another reference round to other fp16 values.  Either
+        # result is within the bound of the 64-bit one.
+        _compare(pages, seqs[:last], q, cu, out, lse, D ** -0.5)
+
+    def changed(a, at, value):
+        a = a.copy()
+        a[at] = value
+        return a
+
+    clean, _, status = run()
+    assert status == 0
+    bad = nvq.NVQ_STATUS_BAD_SEQUENCE
+    for page in (pages.P, -1):
+        pages.table = changed(table, (last, 1), page)
+        out, lse, status = run()
+        pages.table = table
+        assert status == bad
+        others_hold(out, lse)
+    for length in (-5, 2 ** 31 - 1, pages.width * 64 + 1):
+        out, lse, status = run(lens=changed(lens, last, length))
+        assert status == bad
+        others_hold(out, lse)
+    n = int(np.diff(cu).max())
+    for at, value in ((last + 1, cu[-1] + 1), (last + 1, 2 ** 31 - 1), (0, -1), (last + 1, cu[last] - 1)):
+        assert run(cu=changed(cu, at, value), max_q=n)[2] == bad, (at, value)
+    if n > 1:
+        assert run(max_q=n - 1)[2] == bad
+    out, _, status = run()
+    assert status == 0 and torch.equal(out, clean)
+
+
+def test_bad_pages_among_many_sequences_of_many_rows():
+    """More sequences than one step of the check holds, in the 512-thread launch."""
+    nvq = _nvq()
+    seqs = [(2, 3 + i % 60) for i in range(600)]
+    pages = ref.Pages([b for _, b in seqs], 1, 16, 128, seed=4)
+    _table_of(pages, 2048)
+    q, cu, lens = _queries(seqs, 70, 128, 7)
+    ws = nvq.workspace(256 << 20, "cuda")
+    cache, table = pages.cache(nvq), pages.table
+    log("[attention] 600 sequences of 140 rows")
+    _attend(pages, q, cu, lens, cache, ws)
+    assert nvq.device_status(ws) == 0
+    for b in (0, 255, 256, 599):
+        log(f"[attention] bad page in sequence {b}")
+        pages.table = table.copy()
+        pages.table[b, 0] = pages.P
+        _attend(pages, q, cu, lens, cache, ws)
+        assert nvq.device_status(ws) == nvq.NVQ_STATUS_BAD_SEQUENCE, b
