@@ -130,11 +130,11 @@ __global__ __launch_bounds__(256) void k_attn_any(AttnParams p) {
     f[w] = __builtin_amdgcn_exp2f(s_ml[w][0] - ref);
     sum += s_ml[w][1] * f[w];
   }
-  const float inv = sum == 0.0f ? 0.0f : *p.c.v_st / sum;
+  const OutScale scale(sum, *p.c.v_st);
   uint16_t* out = p.out + row * p.out_ld_t + h * p.out_ld_h;
   for (int d = threadIdx.x; d < D; d += 256) {
     const float v = s_o[0][d] * f[0] + s_o[1][d] * f[1] + s_o[2][d] * f[2] + s_o[3][d] * f[3];
-    out[d] = (uint16_t)f32_to_bf16_any(v * inv);
+    out[d] = (uint16_t)scale.bf16(v);
   }
   if (p.lse && threadIdx.x == 0)
     p.lse[(int64_t)row * p.Hq + h] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;

@@ -397,15 +397,15 @@ __global__ __launch_bounds__(64 * W, chunk_wgs_per_cu(D, W) * W / 4) void k_attn
     l += __shfl_xor(l, 32, 64);
     if (whole) {
       if (live) {
-        const float inv = l == 0.0f ? 0.0f : v_st / l;
+        const OutScale scale(l, v_st);
         uint16_t* out = p.out + (s.row0 + qi) * p.out_ld_t + qh * p.out_ld_h;
 #pragma unroll
         for (int i = 0; i < kOut; ++i)
 #pragma unroll
           for (int v = 0; v < 4; ++v)
             *reinterpret_cast<uint2*>(out + 32 * i + 8 * v + 4 * h) =
-                make_uint2(f32_to_bf16_any(o[i][4 * v] * inv) | (f32_to_bf16_any(o[i][4 * v + 1] * inv) << 16),
-                           f32_to_bf16_any(o[i][4 * v + 2] * inv) | (f32_to_bf16_any(o[i][4 * v + 3] * inv) << 16));
+                make_uint2(scale.bf16(o[i][4 * v]) | (scale.bf16(o[i][4 * v + 1]) << 16),
+                           scale.bf16(o[i][4 * v + 2]) | (scale.bf16(o[i][4 * v + 3]) << 16));
         if (p.lse && h == 0)
           p.lse[(int64_t)(s.row0 + qi) * p.Hq + qh] = l == 0.0f ? -INFINITY : (ref + __builtin_log2f(l)) * kLn2;
       }

@@ -77,10 +77,10 @@ __device__ __forceinline__ void join_rows(const AttnParams& p, const float2* par
 #pragma unroll
       for (int e = 0; e < kE; ++e) x[e] += lds.o[v][k][kE * lane + e] * f;
     }
-    const float inv = sum == 0.0f ? 0.0f : *p.c.v_st / sum;
+    const OutScale scale(sum, *p.c.v_st);
     uint16_t* out = p.out + row * p.out_ld_t + head * p.out_ld_h + kE * lane;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) out[e] = (uint16_t)f32_to_bf16_any(x[e] * inv);
+    for (int e = 0; e < kE; ++e) out[e] = (uint16_t)scale.bf16(x[e]);
     if (p.lse && lane == 0)
       p.lse[row * p.Hq + head] = sum == 0.0f ? -INFINITY : (top + __builtin_log2f(sum)) * kLn2;
   }

@@ -494,11 +494,10 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
         }
         if (whole_seq) {
           const int i = r / p.g, h = kvh * p.g + (r - i * p.g);
-          const float inv = sum == 0.0f ? 0.0f : v_st / sum;
+          const OutScale scale(sum, v_st);
           uint32_t w[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            w[j] = f32_to_bf16_any(x[2 * j] * inv) | (f32_to_bf16_any(x[2 * j + 1] * inv) << 16);
+          for (int j = 0; j < 4; ++j) w[j] = scale.bf16(x[2 * j]) | (scale.bf16(x[2 * j + 1]) << 16);
           *reinterpret_cast<uint4*>(p.out + (s.row0 + i) * p.out_ld_t + h * p.out_ld_h + 8 * ch) =
               make_uint4(w[0], w[1], w[2], w[3]);
           if (p.lse && ch == 0)
@@ -520,14 +519,14 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
         if (r >= rows) continue;
         if (whole_seq) {
           const int i = r / p.g, h = kvh * p.g + (r - i * p.g);
-          const float inv = l[mt] == 0.0f ? 0.0f : v_st / l[mt];
+          const OutScale scale(l[mt], v_st);
           uint16_t* out = p.out + (s.row0 + i) * p.out_ld_t + h * p.out_ld_h + 4 * q * kTiles;
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint32_t w[kTiles / 2];
 #pragma unroll
             for (int j = 0; j < kTiles / 2; ++j)
-              w[j] = f32_to_bf16_any(o[mt][2 * j][v] * inv) | (f32_to_bf16_any(o[mt][2 * j + 1][v] * inv) << 16);
+              w[j] = scale.bf16(o[mt][2 * j][v]) | (scale.bf16(o[mt][2 * j + 1][v]) << 16);
             __builtin_memcpy(__builtin_assume_aligned(out + v * kTiles, kTiles < 8 ? 8 : 16), w, sizeof(w));
           }
           if (p.lse && q == 0)

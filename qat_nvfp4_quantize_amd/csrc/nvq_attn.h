@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "nvq.h"
+#include "nvq_device.h"
 #include "nvq_kv.h"
 #include "nvq_scan.h"
 
@@ -70,6 +71,17 @@ int attn_rows_launch(const AttnParams& p, const RowsPlan& plan, const ChunkPlan&
 int attn_join_launch(const AttnParams& p, const RowsPlan* rows, const ChunkPlan* chunk, hipStream_t s);
 
 constexpr float kLn2 = 0.69314718055994530942f;
+
+// An output is a sum of weighted codes over the sum of weights, times V's
+// tensor scale, in two factors: sums of weights pass 2^26, under which their
+// quotient with a small scale is no normal number though the output is one.  No
+// weight at all (no key seen): zeros, whatever the scale.
+struct OutScale {
+  float inv, st;
+  __device__ __forceinline__ OutScale(float sum, float v_st)
+      : inv(sum == 0.0f ? 0.0f : 1.0f / sum), st(sum == 0.0f ? 0.0f : v_st) {}
+  __device__ __forceinline__ uint32_t bf16(float x) const { return f32_to_bf16_any(x * inv * st); }
+};
 
 // Rows and keys of sequence b, cut to what the call's buffers hold.
 struct Seq {

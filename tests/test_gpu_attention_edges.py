@@ -179,3 +179,17 @@ def test_bad_pages_among_many_sequences_of_many_rows():
         pages.table[b, 0] = pages.P
         _attend(pages, q, cu, lens, cache, ws)
         assert nvq.device_status(ws) == nvq.NVQ_STATUS_BAD_SEQUENCE, b
+
+
+@pytest.mark.parametrize("v_st", [2.0 ** -126, 4e-40, 2.0 ** 112])
+@pytest.mark.parametrize("D,Hkv,seqs", KINDS)
+def test_tensor_scales_of_v_far_from_one(D, Hkv, seqs, v_st):
+    """The sum of the weights may pass 2^26: divided by it, a small tensor scale
+    is no normal number, though the output is.  Equal scores make the largest
+    sums.  Outputs under 2^-126 are rounded to multiples of 2^-133 in bf16 (off
+    by 2^-134), after an fp32 product that is off by 2^-150."""
+    log(f"[attention] V scale {v_st} D={D} {len(seqs)} sequences, first {seqs[:2]}")
+    pages = ref.Pages([b for _, b in seqs], Hkv, 16, D, seed=D, v_st=v_st)
+    q, cu, lens = _queries(seqs, 2 * Hkv, D, 3)
+    out, lse = _attend(pages, q, cu, lens, scale=0.0)
+    _compare(pages, seqs, q, cu, out, lse, 0.0, 2.0 ** -134 + 2.0 ** -150)
