@@ -55,11 +55,20 @@ __global__ __launch_bounds__(256) void k_attn_any(AttnParams p) {
   if (row < s.row0 || row >= s.row0 + s.n) return;
   int64_t lo, hi;
   visible(p, s, s.pos0 + (row - s.row0), lo, hi);
+  // Q under a power of two that brings its largest magnitude to 2^14 .. 2^15, as
+  // in the other kernels: its products with stored values stay within fp32.
+  // Every wave looks over the row itself.
   const uint16_t* q = p.q + row * p.q_ld_t + h * p.q_ld_h;
-  for (int d = threadIdx.x; d < D; d += 256) s_q[d] = bf16_to_f32(q[d]);
+  uint32_t big = 0;
+  for (int d = lane; d < D; d += 64) big = max(big, (uint32_t)q[d] & 0x7FFFu);
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) big = max(big, (uint32_t)__shfl_xor((int)big, x, 64));
+  const int ex = (int)(big >> 7);
+  const int shift = (big == 0u || ex == 255) ? 0 : 14 + 127 - max(ex, 1);
+  for (int d = threadIdx.x; d < D; d += 256) s_q[d] = __builtin_ldexpf(bf16_to_f32(q[d]), shift);
   __syncthreads();
   const int32_t* table = p.table + b * p.table_ld;
-  const float c = p.scale_log2 * *p.c.k_st;
+  const float c = __builtin_ldexpf(p.scale_log2 * *p.c.k_st, -shift);
   float m = -INFINITY, l = 0.0f, o[kAnyMaxD / 64];
 #pragma unroll
   for (int i = 0; i < kAnyMaxD / 64; ++i) o[i] = 0.0f;

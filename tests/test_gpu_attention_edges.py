@@ -193,3 +193,17 @@ def test_tensor_scales_of_v_far_from_one(D, Hkv, seqs, v_st):
     q, cu, lens = _queries(seqs, 2 * Hkv, D, 3)
     out, lse = _attend(pages, q, cu, lens, scale=0.0)
     _compare(pages, seqs, q, cu, out, lse, 0.0, 2.0 ** -134 + 2.0 ** -150)
+
+
+@pytest.mark.parametrize("D,Hkv,seqs", KINDS + [(80, 1, [(40, 90), (1, 700)]), (512, 1, [(2, 40), (1, 70)])])
+@pytest.mark.parametrize("power", [124, -124])
+def test_queries_far_from_one(D, Hkv, seqs, power):
+    """Finite queries near either end of bf16's range under a softmax scale that
+    brings the scores back to a few units: no product on the way may leave fp32."""
+    log(f"[attention] queries of 2^{power} D={D} {len(seqs)} sequences, first {seqs[:2]}")
+    pages = ref.Pages([b for _, b in seqs], Hkv, 16, D, seed=D)
+    q, cu, lens = _queries(seqs, 2 * Hkv, D, 5)
+    q = q.clamp(-7.0, 7.0) * 2.0 ** power  # exact, below 2^127
+    scale = 2.0 ** (2 - power) if power > 0 else 2.0 ** 126
+    out, lse = _attend(pages, q, cu, lens, scale=scale)
+    _compare(pages, seqs, q, cu, out, lse, scale)
