@@ -550,6 +550,16 @@ def _on(dev, **tensors):
             raise ValueError(f"{name} must be a GPU tensor on {dev}, got {t.device}")
 
 
+def _ws_args(ws):
+    """(pointer, bytes) of a workspace, which the library writes from its start
+    to its end: a tensor of any type and shape without gaps, or None."""
+    if ws is None:
+        return None, 0
+    if not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous, got {list(ws.shape)}, strides {list(ws.stride())}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _typed(t, name, dtype, *shape):
     """A contiguous tensor of this dtype and (where given) shape."""
     if t.dtype != dtype or not t.is_contiguous() or (shape and t.shape != shape):
@@ -663,8 +673,7 @@ def nvq_kv_append(cache, k, v, slots, ws=None):
     _typed(slots, "slots", torch.int32, T)
     _on(cache.device, k=k, v=v, slots=slots, ws=ws)
     _call((_lib or load()).nvq_kv_append, "nvq_kv_append", cache.device, cache._ref, k.data_ptr(),
-          v.data_ptr(), _dtype_code(k), T, k_t, k_h, v_t, v_h, slots.data_ptr(),
-          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
+          v.data_ptr(), _dtype_code(k), T, k_t, k_h, v_t, v_h, slots.data_ptr(), *_ws_args(ws))
 
 
 def nvq_kv_gather(cache, slots, out_dtype=torch.bfloat16, out=None, ws=None):
@@ -683,8 +692,7 @@ def nvq_kv_gather(cache, slots, out_dtype=torch.bfloat16, out=None, ws=None):
         _typed(v, "v", k.dtype, *shape)
     _on(cache.device, slots=slots, k=k, v=v, ws=ws)
     _call((_lib or load()).nvq_kv_gather, "nvq_kv_gather", cache.device, cache._ref, slots.data_ptr(), T,
-          k.data_ptr(), v.data_ptr(), _dtype_code(k), None if ws is None else ws.data_ptr(),
-          0 if ws is None else ws.numel())
+          k.data_ptr(), v.data_ptr(), _dtype_code(k), *_ws_args(ws))
     return k, v
 
 
@@ -738,7 +746,7 @@ def nvq_paged_attention(q, cache, cu_q, kv_len, block_table, max_q=None, scale=N
                 nbytes = L.nvq_paged_attention_workspace_bytes(cache._ref, args)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _call(L.nvq_paged_attention, "nvq_paged_attention", dev, cache._ref,
-          _ATTENTION.pack(*head, ws.data_ptr(), ws.numel()))
+          _ATTENTION.pack(*head, *_ws_args(ws)))
     return out
 
 

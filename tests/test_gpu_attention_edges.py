@@ -207,3 +207,29 @@ def test_queries_far_from_one(D, Hkv, seqs, power):
     scale = 2.0 ** (2 - power) if power > 0 else 2.0 ** 126
     out, lse = _attend(pages, q, cu, lens, scale=scale)
     _compare(pages, seqs, q, cu, out, lse, scale)
+
+
+def test_workspaces_with_gaps_are_refused_and_of_any_type_taken():
+    """An expanded tensor has more elements than memory: it must not be written.
+    A workspace of another type is as large as its bytes."""
+    import torch
+
+    nvq = _nvq()
+    seqs = [(1, 3000), (2, 40)]
+    pages = ref.Pages([b for _, b in seqs], 2, 16, 128, seed=2)
+    q, cu, lens = _queries(seqs, 8, 128, 3)
+    want, _ = _attend(pages, q, cu, lens)
+    got, _ = _attend(pages, q, cu, lens, ws=torch.empty(4 << 20, dtype=torch.int64, device="cuda"))
+    assert torch.equal(got, want)
+    cache = pages.cache(nvq)
+    x = torch.randn(3, 2, 128, device="cuda")
+    slots = torch.arange(3, dtype=torch.int32, device="cuda")
+    nvq.nvq_kv_append(cache, x, x, slots, ws=torch.empty(64, dtype=torch.int32, device="cuda"))
+    for ws in (torch.empty(256, dtype=torch.uint8, device="cuda")[:1].expand(1 << 28),
+               torch.empty(1 << 20, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            _attend(pages, q, cu, lens, cache, ws)
+        with pytest.raises(ValueError, match="contiguous"):
+            nvq.nvq_kv_append(cache, x, x, slots, ws=ws)
+        with pytest.raises(ValueError, match="contiguous"):
+            nvq.nvq_kv_gather(cache, slots, ws=ws)
