@@ -169,7 +169,10 @@ __device__ __forceinline__ void rescale(floatx16_t (&o)[kN], float keep) {
   }
 }
 
-// Largest of three (v_max3_f32; fmaxf would first quiet each operand).
+// Largest of three (v_max3_f32; fmaxf would first quiet each operand).  The
+// compiler does not look into it: where b and c come out of the matrix unit, `a`
+// has to depend on an ordinary operation on the same sums, before which it puts
+// the wait states that such a read needs.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float m;
   asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(a), "v"(b), "v"(c));
@@ -346,7 +349,8 @@ __global__ __launch_bounds__(64 * W, chunk_wgs_per_cu(D, W) * W / 4) void k_attn
             sc[kt][v] = (key >= see_lo && key < see_hi && !none) ? sc[kt][v] : -INFINITY;
           }
       }
-      float top = max3(sc[0][0], sc[1][0], sc[1][1]), top2 = max3(sc[0][1], sc[0][2], sc[1][2]);
+      const float first = fmaxf(sc[0][0], sc[1][0]);
+      float top = max3(first, sc[0][1], sc[1][1]), top2 = max3(first, sc[0][2], sc[1][2]);
 #pragma unroll
       for (int v = 3; v < 15; v += 2) {
         top = max3(top, sc[0][v], sc[1][v]);
