@@ -14,10 +14,10 @@
 
 #include "nvq.h"
 #include "nvq_attn.h"
+#include "nvq_dequant.h"
 #include "nvq_device.h"
 #include "nvq_internal.h"
 #include "nvq_kv.h"
-#include "nvq_quant_block.h"
 
 namespace nvq {
 namespace {
@@ -82,10 +82,12 @@ __global__ __launch_bounds__(256) void k_attn_any(AttnParams p) {
     if (see) {
       for (int blk = 0; blk < nb; ++blk) {
         const uint2 cw = *reinterpret_cast<const uint2*>(p.c.k_codes + ((tile + off) * nb + blk) * 8);
-        float v[16];
-        block_values(cw, e4m3_to_f32(p.c.k_scales[(tile + off) * nb + blk]), 1.0f, v);
+        const uint32_t s_b = scale_pair(p.c.k_scales[(tile + off) * nb + blk], 0);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dot = fmaf(v[i], s_q[blk * 16 + i], dot);
+        for (int i = 0; i < 16; ++i) {
+          const half8_t v = dequant8(i < 8 ? cw.x : cw.y, s_b);
+          dot = fmaf((float)v[i & 7], s_q[blk * 16 + i], dot);
+        }
       }
     }
     const float sc = see ? dot * c : -INFINITY;
