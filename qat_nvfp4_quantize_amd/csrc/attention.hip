@@ -34,7 +34,7 @@ __global__ __launch_bounds__(256) void k_attn_any(AttnParams p) {
   __shared__ float s_ml[4][2];
   __shared__ CheckLds s_check;
   if (blockIdx.y == 0) {
-    if (blockIdx.x == 0) check_batch(p, s_check);
+    if (blockIdx.x == 0) check_batch<256>(p, s_check);
     return;
   }
   const int row = blockIdx.x, h = blockIdx.y - 1, kvh = h / p.g;

@@ -185,8 +185,8 @@ __global__ __launch_bounds__(64 * W, chunk_wgs_per_cu(D, W) * W / 4) void k_attn
   constexpr int kSteps = D / 16, kOut = D / 32, kTileRows = 32 * W;
   __shared__ Lds lds;
   if (plan.check && blockIdx.x == 0) {
-    static_assert(sizeof(CheckLds) <= sizeof(Lds) && 64 * W >= kCheckBatch);
-    check_batch(p, reinterpret_cast<CheckLds&>(lds));
+    static_assert(sizeof(CheckLds) <= sizeof(Lds));
+    check_batch<64 * W>(p, reinterpret_cast<CheckLds&>(lds));
     return;
   }
   const int block = blockIdx.x - plan.check, kvh = block % p.c.H, run = block / p.c.H;

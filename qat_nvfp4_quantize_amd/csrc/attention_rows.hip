@@ -198,7 +198,7 @@ __global__ __launch_bounds__(256, rows_wgs_per_cu(D, MT)) void k_attn_rows(AttnP
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // one workgroup more than workers, and one that plans the many-rows launch
   if (blockIdx.x == 0) {
-    check_batch(p, s_one.check);
+    check_batch<256>(p, s_one.check);
     return;
   }
   if (plan.plans_chunks && blockIdx.x == 1) {

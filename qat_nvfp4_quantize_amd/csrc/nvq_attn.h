@@ -111,8 +111,8 @@ __device__ __forceinline__ void visible(const AttnParams& p, const Seq& s, int64
 // stay inside the buffers, so no atomic and no clearing is needed.  A batch
 // of 256 sequences at a time, a thread each, then the pages of all of them in
 // one run, so that few loads wait for one another (64 sequences of 64 pages:
-// 17 us with a loop over the sequences, hidden now).  Every thread of the
-// workgroup calls it, 256 or more: those past the batch add nothing to the scan.
+// 17 us with a loop over the sequences, hidden now).  All kThreads threads of
+// the workgroup call it: those past the batch add nothing to the scan.
 constexpr int kCheckBatch = 256;
 struct CheckLds {
   int end[kCheckBatch];  // pages of the batch's sequences up to and with this one
@@ -120,9 +120,11 @@ struct CheckLds {
   int wave[16];
   uint32_t flag;
 };
+template <int kThreads>
 __device__ __forceinline__ void check_batch(const AttnParams& p, CheckLds& lds) {
+  static_assert(kThreads >= kCheckBatch);
   const int t = threadIdx.x;
-  const bool in_batch = t < kCheckBatch;
+  const bool in_batch = kThreads == kCheckBatch || t < kCheckBatch;
   if (t == 0) lds.flag = 0u;
   bool bad = false;
   for (int b0 = 0; b0 < p.B; b0 += kCheckBatch) {
@@ -149,7 +151,7 @@ __device__ __forceinline__ void check_batch(const AttnParams& p, CheckLds& lds) 
     __syncthreads();
     const int all = lds.end[kCheckBatch - 1];
 #pragma unroll 4
-    for (int i = t; i < all; i += blockDim.x) {
+    for (int i = t; i < all; i += kThreads) {
       int lo = 0, hi = kCheckBatch - 1;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
