@@ -431,9 +431,9 @@ int qat_fakequant_gemm_w4a16(const nvq_qat_gemm_args* args, void* stream);
  *           is required; 16-byte aligned rows with rot_dim % 16 == 0 (bf16) or
  *           % 8 (fp32), D a multiple of 8 (bf16) or 4, take the vector path.
  * positions [T] int32, any value.  inv_freq [rot_dim / 2] fp64, radians per
- *           position.  Angles are reduced in fp64 (their error stays below
- *           2^-20 radians at every int32 position), sine, cosine and the
- *           products are fp32, rounded once to dtype.
+ *           position.  Angles are reduced in fp64 (for frequencies up to 1
+ *           their error stays below 2^-20 radians at every int32 position),
+ *           sine, cosine and the products are fp32, rounded once to dtype.
  * 2 <= rot_dim <= D <= 4096, rot_dim even, H <= 65535, T < 2^24; the
  * rows of y do not overlap.
  * Asynchronous on stream; errors (NVQ_EINVAL, NVQ_ESHAPE, NVQ_EALIGN) launch
@@ -455,6 +455,8 @@ int nvq_rope(const void* x, int dtype, int64_t T, int64_t H, int64_t D, int64_t 
  *                    (fast - slow), 0, 1) with n_j = orig_len f_j / (2 pi) the
  *                    pair's turns over the original context (0 < slow < fast);
  *                    *magnitude = 0.1 ln(factor) + 1.
+ * The ramp is linear in the pairs' turns.  A checkpoint that was stretched with
+ * another ramp (one linear in the pair index, say) brings its own inv_freq.
  * *magnitude (nullable) is 1 for the other kinds.  factor >= 1, base > 0 (> 1
  * for NVQ_ROPE_BASE).  No HIP call.  NVQ_EINVAL / NVQ_ESHAPE. */
 enum { NVQ_ROPE_PLAIN = 0, NVQ_ROPE_LINEAR = 1, NVQ_ROPE_BASE = 2, NVQ_ROPE_RAMP = 3 };
@@ -525,9 +527,14 @@ int nvq_kv_gather(const nvq_kv_cache* cache, const int32_t* slots, int64_t T, vo
  * and j > p - window if window > 0 (causal only).  A row without visible keys
  * gives zeros and lse = -inf.  lse [total_q, q_heads] (nullable) receives the
  * natural logarithm of the sum of exponentials.
- * q is bf16; q . K^ is summed in fp32 from exact products (q is held in fp16
- * under a power of two per row), the softmax is fp32, its weights are rounded
- * to fp16 for the product with V^ (2^-11 relative), out is rounded to bf16.
+ * q is bf16.  For head dimensions 64, 128 and 256 it is held in fp16 under a
+ * power of two per row and head, which is exact for elements down to 2^-31 of
+ * the largest and off by at most 2^-39 of it for smaller ones; q . K^ is summed
+ * in fp32 from exact products, the softmax is fp32, its weights are rounded to
+ * fp16 for the product with V^ (2^-11 relative), out is rounded to bf16.  Other
+ * head dimensions keep q and the weights in fp32.  A query that holds a NaN
+ * gives NaN, out and lse, if its row sees a key; scores of -inf weigh nothing,
+ * and a row that has no others counts as one without visible keys.
  *
  * Rows that no sequence owns (before cu_q[0], from cu_q[B] on) are not
  * written.  A page id outside [0, num_pages), keys past the block table's
@@ -541,7 +548,8 @@ int nvq_kv_gather(const nvq_kv_cache* cache, const int32_t* slots, int64_t T, vo
 typedef struct nvq_paged_attention_args {
   size_t struct_size;          /* sizeof(nvq_paged_attention_args) */
   int64_t total_q, B;          /* query rows; sequences */
-  int64_t max_q;               /* no sequence has more new tokens; 0: total_q */
+  int64_t max_q;               /* no sequence has more new tokens; 0: total_q.  It and the table's
+                                  width choose the kernels: values near the batch's own are faster */
   int32_t q_heads;             /* a multiple of cache->heads */
   int32_t causal;              /* 0 or 1 */
   int64_t window;              /* 0: none */

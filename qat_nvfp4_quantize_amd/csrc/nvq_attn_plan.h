@@ -12,14 +12,15 @@ namespace nvq {
 
 constexpr int kTileKeys = 64;
 constexpr int kChunkMinUnits = 2;  // key tiles of a run, at least
-// Row tiles go out whole, those with most keys first, or their units are dealt
-// in equal runs, whose divided tiles leave parts that the join reads: about 4
-// units' time, and 16 more if all places take part.  With this many tiles per
-// place they go out whole in any case; with fewer, whichever is expected to take
-// less: 1000 new tokens, 32 heads on 8 of 128, 39 us whole against 71; 79 behind
-// 1116 of one head of 256 31 us divided against 60.  A workgroup alone on a CU
-// that holds more takes kLonePace of a unit's time (1523 new tokens, 16 heads on
-// 4 of 64: 46 us whole against 68).
+// Row tiles go out whole (sequences in the batch's order; within one the last
+// rows, which see the most keys, first), or their units are dealt in equal runs,
+// whose divided tiles leave parts that the join reads: about 4 units' time, and
+// 16 more if all places take part.  With this many tiles per place they go out
+// whole in any case, also where one tile is far longer than the others; with
+// fewer, whichever is expected to take less: 1000 new tokens, 32 heads on 8 of
+// 128, 39 us whole against 71; 79 behind 1116 of one head of 256 31 us divided
+// against 60.  A workgroup alone on a CU that holds more takes kLonePace of a
+// unit's time (1523 new tokens, 16 heads on 4 of 64: 46 us whole against 68).
 constexpr float kWholeTiles = 1.5f, kJoinUnits = 4, kPartUnits = 16, kLonePace = 0.6f;
 
 // Keys of row tile qt of sequence s, in 64-key tiles from `base`.

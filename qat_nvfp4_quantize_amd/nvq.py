@@ -600,7 +600,8 @@ def nvq_rope(x, positions, inv_freq, interleaved=False, magnitude=1.0, inverse=F
     """x [T, H, D] (bf16/fp32, tokens and heads may be strided) with the first
     2 * len(inv_freq) elements of each head turned by positions [T] int32 times
     inv_freq (fp64, on the GPU); inverse turns back (the gradient).  out: a
-    tensor like x to write, x itself for in place."""
+    tensor like x to write, x itself for in place.  Like every call here it is
+    not recorded for autograd: the gradient is the inverse call."""
     T, H, D, ld_t, ld_h = _heads(x, "x")
     dev = x.device
     old_t = old_h = 0
@@ -664,7 +665,8 @@ class KvCache:
 def nvq_kv_append(cache, k, v, slots, ws=None):
     """Quantizes the new tokens k, v [T, heads, D] (bf16/fp32, tokens and heads
     may be strided) into the cache's slots [T] int32 (page * page_size + offset,
-    negative: skipped).  ws (optional, >= 256 bytes) receives the status word."""
+    negative: skipped).  Bad slots and non-finite values raise nothing: they
+    show in device_status(ws) of a caller's ws (>= 256 bytes)."""
     T, H, D, k_t, k_h = _heads(k, "k")
     _, _, _, v_t, v_h = _heads(v, "v")
     if k.shape != v.shape or k.dtype != v.dtype or H != cache.heads or D != cache.head_dim:
@@ -678,7 +680,8 @@ def nvq_kv_append(cache, k, v, slots, ws=None):
 
 def nvq_kv_gather(cache, slots, out_dtype=torch.bfloat16, out=None, ws=None):
     """(k, v) [T, heads, D] read back from the cache's slots [T] int32 (a
-    negative slot: zeros).  ws (optional) receives the status word."""
+    negative slot: zeros).  Bad slots raise nothing (zeros): they show in
+    device_status(ws) of a caller's ws (>= 256 bytes)."""
     T = slots.numel()
     _typed(slots, "slots", torch.int32, T)
     shape = (T, cache.heads, cache.head_dim)
@@ -702,10 +705,15 @@ def nvq_paged_attention(q, cache, cu_q, kv_len, block_table, max_q=None, scale=N
     heads may be strided) over the cache: sequence b owns rows cu_q[b] ..
     cu_q[b + 1] - 1 and keys 0 .. kv_len[b] - 1, in the pages block_table[b].
     cu_q [B + 1], kv_len [B], block_table [B, width] int32 (rows may be
-    strided).  max_q: no sequence has more new tokens (default: all of them).
-    scale defaults to D^-1/2.  lse: optional fp32 [total_q, q_heads] to receive
-    the log-sum-exp.  ws: a workspace to reuse (default: one for the call).
-    Returns out, bf16 like q."""
+    strided).  max_q: no sequence has more new tokens (default: total_q, which
+    plans a decode batch like prompts: pass 1 there).  scale defaults to D^-1/2.
+    lse: optional fp32 [total_q, q_heads] to receive the log-sum-exp.  ws: a
+    workspace to reuse (default: one for the call).  Returns out, bf16 like q.
+
+    Rows that no sequence owns (padding before cu_q[0] or from cu_q[B] on, and a
+    sequence's rows past max_q) are not written: without `out` they hold
+    whatever the allocation did.  Mistakes in the index arrays raise nothing:
+    they set a bit that only device_status(ws) of a caller's ws shows."""
     T, Hq, D, ld_t, ld_h = _heads(q, "q", (torch.bfloat16,))
     dev = cache.device
     if D != cache.head_dim:
