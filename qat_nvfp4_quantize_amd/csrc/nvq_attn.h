@@ -72,10 +72,10 @@ int attn_join_launch(const AttnParams& p, const RowsPlan* rows, const ChunkPlan*
 
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// An output is a sum of weighted codes over the sum of weights, times V's
-// tensor scale, in two factors: sums of weights pass 2^26, under which their
-// quotient with a small scale is no normal number though the output is one.  No
-// weight at all (no key seen): zeros, whatever the scale.
+// An output is a sum of weighted codes divided by the sum of weights, times V's
+// tensor scale.  In two factors: sums of weights pass 2^26, and a small scale
+// divided by that is no normal number though the output is one.  No weight at
+// all (no key seen): zeros, whatever the scale.
 struct OutScale {
   float inv, st;
   __device__ __forceinline__ OutScale(float sum, float v_st)
