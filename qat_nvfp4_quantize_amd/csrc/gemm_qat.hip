@@ -941,13 +941,14 @@ constexpr int G_STAGE = G_DY + G_X + G_TOK;
 // Global -> LDS direct loads; lane l lands at LDS byte lds_addr + size * l.
 // lds_addr must be wave-uniform; it is read from the first lane so that it
 // is in a scalar register even where the compiler cannot prove uniformity.
+// m0 is read one wait state after its write at the earliest.
 __device__ __forceinline__ void dma16(const void* g, uint32_t lds_addr) {
   const uint32_t m = __builtin_amdgcn_readfirstlane(lds_addr);
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(m) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(m) : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(const void* g, uint32_t lds_addr) {
   const uint32_t m = __builtin_amdgcn_readfirstlane(lds_addr);
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(m) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(m) : "memory", "m0");
 }
 
 __global__ __launch_bounds__(512, 1) void k_qat_wgrad2(QatParams p) {

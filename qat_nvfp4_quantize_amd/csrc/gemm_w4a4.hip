@@ -370,10 +370,11 @@ __device__ __forceinline__ int64_t loader_b_row(const GemmParams& p, const TileC
 // lds_addr + 16 l (lds_addr wave-uniform, read from the first lane).  Issued
 // from inline assembly, so the compiler places no wait for it in front of
 // unrelated LDS reads; the reader waits (vmcnt) and synchronizes itself.
+// m0 is read one wait state after its write at the earliest.
 #define NVQ_LDS_U8 __attribute__((address_space(3))) uint8_t
 __device__ __forceinline__ void dma16_lds(const void* g, uint32_t lds_addr) {
   const uint32_t m = __builtin_amdgcn_readfirstlane(lds_addr);
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(m) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(m) : "memory", "m0");
 }
 
 // The compensation operands of the first 128-channel step, fetched while
