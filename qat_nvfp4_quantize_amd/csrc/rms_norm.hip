@@ -353,7 +353,7 @@ __global__ __launch_bounds__(Group<kL>::kThreads) void k_rms_norm(NormParams p) 
       f[j] *= s.inverse;
       again |= near_midpoint(f[j]) ? 1u << j : 0u;
     }
-    if (s.stored == kLeastScale) again = 0;
+    if (!(s.stored > kLeastScale)) again = 0;  // nor a NaN's: its low bits mean nothing
     if (v < nvec) {
       if (v % lanes == 0) p.scales[t * (p.D / p.group) + v / lanes] = s.stored;
       store_e4m3(p.y8 + t * p.D + 8 * (int64_t)v, f);
@@ -377,7 +377,7 @@ __global__ __launch_bounds__(Group<kL>::kThreads) void k_rms_norm(NormParams p) 
         again |= near_midpoint(f[j]) ? 1u << j : 0u;
       }
       store_e4m3(p.y8 + t * p.D + 8 * (int64_t)v, f);
-      if (s.stored != kLeastScale) decide(k, again, row_product);
+      if (s.stored > kLeastScale) decide(k, again, row_product);
     }
   }
   if (p.amax) {

@@ -317,3 +317,39 @@ def test_graph_replays_and_another_stream():
             assert torch.equal(a, b), rep
         step()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("group", [128, 32, 0])
+@pytest.mark.parametrize("dtype,bits", [("bfloat16", 0x7FC8), ("bfloat16", 0x7FF8), ("bfloat16", -0x0038),
+                                        ("float32", 0x7FC80000), ("float32", 0x7FF80003), ("float32", -0x0037FFFE)])
+def test_eight_bit_nan_of_any_payload(group, dtype, bits):
+    """A NaN keeps its payload through the products; one that looks like a
+    midpoint of the format in its low bits is a NaN all the same."""
+    import torch
+
+    nvq = _nvq()
+    log(f"[norm e4m3 nan] group={group} {dtype} {bits:#x}")
+    T, D = 5, 512
+    x, res, _, _, w = _inputs(T, D, dtype, "float32", seed=21)
+    word = torch.int16 if dtype == "bfloat16" else torch.int32
+    clean, clean_scales, _, _ = nvq.nvq_rms_norm_e4m3(x, w, group=group)
+    bad = x.clone()
+    bad.view(word)[2, 77] = bits
+    assert bool(bad[2, 77].isnan())
+    codes, scales, _, _ = nvq.nvq_rms_norm_e4m3(bad, w, group=group)
+    assert bool(codes[2].float().isnan().all()) and bool(scales[2].isnan().all())
+    rest = [0, 1, 3, 4]
+    assert torch.equal(codes[rest].view(torch.uint8), clean[rest].view(torch.uint8))
+    assert torch.equal(scales[rest], clean_scales[rest])
+    # one weight: its groups, and no other
+    w2 = w.to(getattr(torch, dtype))
+    clean, clean_scales, _, _ = nvq.nvq_rms_norm_e4m3(x, w2, group=group)
+    w2 = w2.clone()
+    w2.view(word)[200] = bits
+    codes, scales, _, _ = nvq.nvq_rms_norm_e4m3(x, w2, group=group)
+    n = group or D
+    hit = torch.arange(D // n, device="cuda") == 200 // n
+    c = codes.view(torch.uint8).reshape(T, D // n, n)
+    assert bool(codes.float().reshape(T, D // n, n)[:, hit].isnan().all()) and bool(scales[:, hit].isnan().all())
+    assert torch.equal(c[:, ~hit], clean.view(torch.uint8).reshape(T, D // n, n)[:, ~hit])
+    assert torch.equal(scales[:, ~hit], clean_scales[:, ~hit])
