@@ -593,8 +593,8 @@ int nvq_paged_attention(const nvq_kv_cache* cache, const nvq_paged_attention_arg
  * The sum of squares is fp64, r and the products fp32, y is rounded once.
  * x, residual, h, y  [T, D] of dtype NVQ_F32 or NVQ_BF16, row strides in
  *   elements (0: D), rows 16-byte aligned.  h is written only with a residual
- *   (required then) and may be x or residual with the same stride; y may be any
- *   of the three with the same stride, except h where h is wanted.
+ *   (required then) and may be x or residual with the same stride; so may y, but
+ *   it may not be h too (NVQ_EINVAL).
  * weight  [D] of w_dtype (either type), 16-byte aligned.
  * y8      nullable [T, D] E4M3 codes (8-byte aligned), dense, with y8_scales fp32
  *   [T, D / group], or [T] for group == 0 (one scale a row): scale = max|y| of

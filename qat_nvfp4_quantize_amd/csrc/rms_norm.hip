@@ -606,6 +606,7 @@ extern "C" int nvq_rms_norm(const nvq_rms_norm_args* a, void* stream) {
   if (p.x_ld < a->D || p.res_ld < a->D || p.h_ld < a->D || p.y_ld < a->D) return NVQ_ESHAPE;
   if (!a->weight) return NVQ_EINVAL;
   if (a->T != 0 && (!a->x || (a->residual && !a->h) || (!a->y && !a->y8) || (a->y8 && !a->y8_scales))) return NVQ_EINVAL;
+  if (a->T != 0 && a->residual && a->y == a->h) return NVQ_EINVAL;  // y would take h's place
   if (!row_ok(a->x, p.x_ld, size) || !row_ok(a->residual, p.res_ld, size) || !row_ok(a->h, p.h_ld, size) ||
       !row_ok(a->y, p.y_ld, size) || !aligned16(a->weight) || ((uintptr_t)a->y8 & 7u) || ((uintptr_t)a->y8_scales & 3u) ||
       ((uintptr_t)a->rstd & 3u) || ((uintptr_t)a->out_amax & 3u))

@@ -187,3 +187,13 @@ def test_binding_refuses_before_the_library():
                  lambda: nvq.nvq_grad_norm([x]), lambda: nvq.nvq_clip_grad_norm([x], 1.0)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_norm_refuses_one_buffer_for_both_results():
+    """y over h would leave the residual stream normalised."""
+    other = OK_PTR + 0x10000
+    assert _norm(residual=other, h=OK_PTR, y=OK_PTR) == EINVAL
+    assert _norm(residual=OK_PTR, h=OK_PTR, y=OK_PTR) == EINVAL
+    assert _norm(residual=OK_PTR, h=OK_PTR, y=OK_PTR, y8=other, y8_scales=other) == EINVAL
+    # nothing is written: not a conflict
+    assert _norm(T=0, residual=other, h=OK_PTR, y=OK_PTR) == 0
