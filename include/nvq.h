@@ -737,12 +737,12 @@ typedef struct nvq_tensor_list {
  *   out_i = grads_i min(1, max_norm / norm)
  * rounded to its type: in place with out == NULL (gradients within max_norm
  * are then not touched), else into tensors of the same sizes and types.  A
- * norm that is not finite scales nothing (out receives the gradients as they
- * are) and sets NVQ_STATUS_NONFINITE.  max_norm >= 0; infinity never clips.
- * Tensors that are written overlap no other of the call (NVQ_EINVAL), but out_i
- * may be grads_i.  A captured graph keeps the tensors' addresses.  Asynchronous on
- * stream; errors (NVQ_EINVAL, NVQ_ESHAPE, NVQ_EALIGN, NVQ_EWORKSPACE) launch
- * nothing. */
+ * norm[0] that is not finite (one past the largest fp32 number too) scales
+ * nothing (out receives the gradients as they are) and sets
+ * NVQ_STATUS_NONFINITE.  max_norm >= 0; infinity never clips.  Tensors that are
+ * written overlap no other of the call (NVQ_EINVAL), but out_i may be grads_i.  A
+ * captured graph keeps the tensors' addresses.  Asynchronous on stream; errors
+ * (NVQ_EINVAL, NVQ_ESHAPE, NVQ_EALIGN, NVQ_EWORKSPACE) launch nothing. */
 size_t nvq_grad_norm_workspace_bytes(const nvq_tensor_list* grads);
 int nvq_grad_norm(const nvq_tensor_list* grads, float* norm, void* ws, size_t ws_bytes, void* stream);
 int nvq_clip_grad_norm(const nvq_tensor_list* grads, const nvq_tensor_list* out, float max_norm,

@@ -1,7 +1,8 @@
 // Global gradient norm over many tensors, and clipping.
 //
 //   norm = sqrt(sum of squares over every element of every tensor)
-//   out  = g min(1, max_norm / norm); a norm that is not finite leaves g as it is
+//   out  = g min(1, max_norm / norm); a norm that is not finite (in fp32, as it is
+//   handed out) leaves g as it is
 //
 // Bound by HBM: the norm needs every element before the first result can be
 // written, so a clipped list is read twice and written once (300 tensors, 1.33
@@ -144,14 +145,18 @@ __device__ __forceinline__ double total_of(const double* part, int n) {
   return block_sum(sum, s);
 }
 
+// Whether the norm that the caller gets, in fp32, is a number: one past the
+// largest is none, whatever fp64 still holds.
+__device__ __forceinline__ bool finite_norm(double norm) { return __builtin_isfinite((float)norm); }
+
 __device__ __forceinline__ float coef_of(double norm, float max_norm) {
-  return norm - norm == 0.0 && norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.0f;
+  return finite_norm(norm) && norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.0f;
 }
 
 __device__ __forceinline__ void report(double norm, float max_norm, float* out, float* coef, uint32_t* status) {
   *out = (float)norm;
   *coef = coef_of(norm, max_norm);
-  *status = norm - norm == 0.0 ? 0u : (uint32_t)NVQ_STATUS_NONFINITE;
+  *status = finite_norm(norm) ? 0u : (uint32_t)NVQ_STATUS_NONFINITE;
 }
 
 __global__ __launch_bounds__(kThreads) void k_norm(const double* part, int n, float max_norm, float* norm, float* coef,

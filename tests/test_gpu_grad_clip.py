@@ -211,3 +211,28 @@ def test_graph_replays_over_changing_gradients():
             m = float(nvq.nvq_clip_grad_norm(grads, 10.0, ws=ws))
         torch.cuda.current_stream().wait_stream(side)
         assert n == m and all(torch.equal(a, b) for a, b in zip(got, grads.tensors)), k
+
+
+def test_a_norm_past_the_largest_number_scales_nothing():
+    """The norm is handed out in fp32: where it is infinite there, although no
+    gradient is, nothing is scaled and the status says so."""
+    import torch
+
+    nvq = _nvq()
+    ws = nvq.workspace(1 << 20, "cuda")
+    for dtype in (torch.float32, torch.bfloat16):
+        grads = [torch.full((37,), 3e38, device="cuda").to(dtype), torch.ones(500, device="cuda", dtype=dtype)]
+        before = [t.clone() for t in grads]
+        outs = [torch.zeros_like(t) for t in grads]
+        assert math.isinf(float(nvq.nvq_grad_norm(grads, ws=ws))) and nvq.device_status(ws) == nvq.NVQ_STATUS_NONFINITE
+        assert math.isinf(float(nvq.nvq_clip_grad_norm(grads, 1.0, out=outs, ws=ws)))
+        assert nvq.device_status(ws) == nvq.NVQ_STATUS_NONFINITE
+        nvq.nvq_clip_grad_norm(grads, 1.0, ws=ws)
+        assert nvq.device_status(ws) == nvq.NVQ_STATUS_NONFINITE
+        for a, b, c in zip(grads, before, outs):
+            assert torch.equal(a, b) and torch.equal(c, b)
+        # the largest norm that is a number still clips
+        grads = [torch.full((1,), 3e38, device="cuda").to(dtype)]
+        norm = float(nvq.nvq_clip_grad_norm(grads, 1.0, ws=ws))
+        assert math.isfinite(norm) and nvq.device_status(ws) == 0
+        assert abs(float(grads[0][0]) - 1.0) <= 2 * ref.round_error(dtype)
