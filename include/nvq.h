@@ -738,7 +738,7 @@ typedef struct nvq_tensor_list {
  * rounded to its type: in place with out == NULL (gradients within max_norm
  * are then not touched), else into tensors of the same sizes and types.  A
  * norm[0] that is not finite (one past the largest fp32 number too) scales
- * nothing (out receives the gradients as they are) and sets
+ * nothing (out receives the gradients bit by bit) and sets
  * NVQ_STATUS_NONFINITE.  max_norm >= 0; infinity never clips.  Tensors that are
  * written overlap no other of the call (NVQ_EINVAL), but out_i may be grads_i.  A
  * captured graph keeps the tensors' addresses.  Asynchronous on stream; errors

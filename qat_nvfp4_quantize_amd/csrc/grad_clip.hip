@@ -178,11 +178,12 @@ __global__ __launch_bounds__(kThreads) void k_scale(Table t, uint32_t chunks, co
   } else {
     c = *coef;
   }
+  const bool scaled = c != 1.0f;  // else bits are copied: a product would change a NaN's
   for (uint32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
     const Piece p = piece_of(t, k);
     const void* const in = t.in[p.tensor];
     void* const out = t.out[p.tensor];
-    if (in == out && c == 1.0f) continue;  // nothing changes
+    if (in == out && !scaled) continue;  // nothing changes
     const int size = p.bf16 ? 2 : 4, per = 16 / size;
     const uint4* const vec = reinterpret_cast<const uint4*>(static_cast<const char*>(in) + p.span.head * size);
     char* const ov = static_cast<char*>(out) + p.span.head * size;
@@ -191,7 +192,7 @@ __global__ __launch_bounds__(kThreads) void k_scale(Table t, uint32_t chunks, co
       const uint4 q = vec[v];
       uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4 && scaled; ++j)
         w[j] = p.bf16 ? f32_to_bf16_any(bf16_lo(w[j]) * c) | (f32_to_bf16_any(bf16_hi(w[j]) * c) << 16)
                       : __float_as_uint(__uint_as_float(w[j]) * c);
       if (aligned) {
@@ -208,6 +209,11 @@ __global__ __launch_bounds__(kThreads) void k_scale(Table t, uint32_t chunks, co
       }
     }
     auto one = [&](int64_t i) {
+      if (!scaled) {
+        if (p.bf16) static_cast<uint16_t*>(out)[i] = static_cast<const uint16_t*>(in)[i];
+        else static_cast<uint32_t*>(out)[i] = static_cast<const uint32_t*>(in)[i];
+        return;
+      }
       const float v = element(in, i, p.bf16) * c;
       if (p.bf16) static_cast<uint16_t*>(out)[i] = (uint16_t)f32_to_bf16_any(v);
       else static_cast<float*>(out)[i] = v;

@@ -236,3 +236,24 @@ def test_a_norm_past_the_largest_number_scales_nothing():
         norm = float(nvq.nvq_clip_grad_norm(grads, 1.0, ws=ws))
         assert math.isfinite(norm) and nvq.device_status(ws) == 0
         assert abs(float(grads[0][0]) - 1.0) <= 2 * ref.round_error(dtype)
+
+
+@pytest.mark.parametrize("offset", [0, 1])
+def test_gradients_that_are_not_scaled_come_bit_by_bit(offset):
+    """NaN payloads, signalling ones and their signs among them, into aligned and
+    unaligned results, in vectors and in the elements beside them."""
+    import torch
+
+    nvq = _nvq()
+    for dtype, word, specials in (
+            (torch.bfloat16, torch.int16, [0x7FC8, 0x7F81, -0x007F, -0x0001, 0x7F80, -0x0080, 0x0001, -0x8000]),
+            (torch.float32, torch.int32, [0x7FC80000, 0x7F800001, -0x007FFFFF, -1, 0x7F800000, -0x00800000, 1, -0x80000000])):
+        g = torch.Generator().manual_seed(2)
+        t = torch.randn(1003, generator=g).to(dtype).cuda()
+        bits = t.view(word)
+        bits[:8] = torch.tensor(specials, dtype=word)
+        bits[500:508] = torch.tensor(specials, dtype=word)
+        bits[-8:] = torch.tensor(specials, dtype=word)
+        out = torch.zeros(1003 + offset, dtype=dtype, device="cuda")[offset:]
+        nvq.nvq_clip_grad_norm([t], 1e-3, out=[out])
+        assert torch.equal(out.view(word), bits)
