@@ -197,3 +197,45 @@ def test_norm_refuses_one_buffer_for_both_results():
     assert _norm(residual=OK_PTR, h=OK_PTR, y=OK_PTR, y8=other, y8_scales=other) == EINVAL
     # nothing is written: not a conflict
     assert _norm(T=0, residual=other, h=OK_PTR, y=OK_PTR) == 0
+
+
+def test_clipping_allocates_nothing():
+    """Where no memory is to be had a long list is judged as ever: accepted up to
+    the workspace that is missing, or refused for its overlap."""
+    import os
+    import subprocess
+    import sys
+
+    _lib()
+    program = """
+import ctypes, resource, sys
+import numpy as np
+from qat_nvfp4_quantize_amd import nvq
+L = nvq.load()
+n = 1 << 18
+size = np.full(n, 16, np.int64)
+kind = np.zeros(n, np.int32)
+order = np.random.default_rng(1).permutation(n)
+
+def listed(at):
+    return nvq.TensorListArgs(ctypes.sizeof(nvq.TensorListArgs), n, at.ctypes.data_as(ctypes.POINTER(ctypes.c_void_p)),
+                              size.ctypes.data_as(ctypes.POINTER(ctypes.c_int64)), kind.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)))
+
+a = (0x100000 + 64 * order).astype(np.uint64)
+b = a + np.uint64(64 * n)
+late = b.copy()
+late[n // 2] = a[n // 3] + np.uint64(60)
+up, above = np.sort(a), np.sort(b)
+tail = above.copy()
+tail[0] -= np.uint64(4)
+lists = [listed(v) for v in (a, b, late, up, above, tail)]
+used = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (used + (2 << 20),) * 2)
+ws = ctypes.c_void_p(0x100000)
+got = [L.nvq_clip_grad_norm(ctypes.byref(lists[i]), None if o is None else ctypes.byref(lists[o]), 1.0, ws, None, 0, None)
+       for i, o in ((0, None), (0, 0), (0, 1), (0, 2), (3, None), (3, 3), (3, 4), (3, 5), (5, 3), (3, 0))]
+sys.exit(0 if got == [-4, -4, -4, -1, -4, -4, -4, -1, -1, -1] else repr(got))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", program], capture_output=True, text=True, cwd=root)
+    assert r.returncode == 0, r.stderr[-500:]
