@@ -681,11 +681,12 @@ int nvq_rms_norm_backward(const nvq_rms_norm_grad_args* args, void* stream);
  *   dw[v] = scale sum_t c[t, v] dloss[t] x[t]   [V, D] of dw_dtype (NVQ_BF16 or
  *           NVQ_F32), nullable, stride dw_ld; added to with accumulate
  * Tokens without a valid target or with dloss == 0 do not count: their dx is 0
- * and nothing they hold reaches dw.  c is computed in fp32 and rounded to bf16
- * (at most 2^-8 relative for each entry), and so is x times dloss over the
- * largest finite |dloss|, which dw's sums take (exact where all weights are
- * equal; where they are not, a target's own term of dw is still good to 2^-15);
- * all sums are fp32, dx and dw are rounded once.  dx and dw overlap
+ * and nothing they hold reaches dw.  c times the mantissa of dloss over the
+ * largest finite |dloss| is computed in fp32 and rounded to bf16 (at most 2^-8
+ * relative for each entry; powers of two of the weights are exact, and where
+ * weights are not a power of two apart, what a target's own terms of dx and dw
+ * lose is added again: they are good to 2^-15); all sums are fp32, dx and dw are
+ * rounded once.  dx and dw overlap
  * nothing else of the call.  Results do not depend on the order in which
  * workgroups run.
  * 8 <= D <= 65536, D % 8 == 0; 1 <= V <= 2^24; T <= 2^23; T V <= 2^39 (each

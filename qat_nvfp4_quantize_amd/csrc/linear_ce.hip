@@ -5,20 +5,20 @@
 //   lse[t]  = ln sum_v exp z[t, v],  loss[t] = lse[t] - z[t, y_t]
 //   c[t, v] = exp(z[t, v] - lse[t]) - [v = y_t]
 //   dx[t]   = scale dloss_t sum_v c[t, v] w[v]
-//   dw[v]   = scale g sum_t c[t, v] (dloss_t / g) x[t],  g = max |dloss|
+//   dw[v]   = scale sum_t c[t, v] dloss_t x[t]
 //
 // Forward: every 256 x 256 tile of logits leaves a maximum and a sum of
 // exponentials per token, which one pass joins.  Gradient: the tokens that
 // count (a valid target, dloss not 0) are gathered into a dense copy first, so
 // padded tokens cost nothing and nothing they hold (NaN included) reaches the
-// sums.  The vocabulary then goes by in pieces: logits again, c rounded to
-// bf16 (2^-8 relative at most; the entries of improbable targets, which carry
-// most of the gradient, round to -1 with hardly any error), and the two
-// products of c with w and with the weighted x.  A token's weight is applied
-// to its row of dx in fp32 and, divided by g, to its row of x in bf16 (exact
-// where all weights are equal, as in a mean loss; where they are not, what the
-// rounding took from a target's own term of dw is added again).  dx is summed in
-// fp32 over the pieces.
+// sums.  A token's weight dloss / g is split into m 2^e, 1 <= m < 2: m goes into
+// c, 2^e with the sign into the token's row of x (exactly) and of dx.  The
+// vocabulary then goes by in pieces: logits again, m c rounded to bf16 (2^-8
+// relative at most, the only rounding to fewer bits on the way to dx and dw; the
+// entries of improbable targets, which carry most of the gradient, round to -1
+// with hardly any error where m is 1, as in a mean loss; where weights differ,
+// what the rounding took from a target's own terms is added again), and the two
+// products of m c with w and with 2^e x.  dx is summed in fp32 over the pieces.
 //
 // Bound by the matrix cores' power: 8192 tokens, 65536 words of 4096 (four
 // products of 4.4 TFLOP) take 3.3 + 10.5 ms, 1.27 PFLOP/s over all of it, the
@@ -47,16 +47,16 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // What the gradient's kernels read of the tokens that count.
 struct Live {
   int32_t* count;   // [1]
-  float* g;         // [1] max |dloss|
+  float* g;         // [1] max |dloss|; dloss / g = m 2^e, 1 <= m < 2, and a sign
   int32_t* row;     // [T] token of live row i
   int32_t* pos;     // [T] live row of a token, or -1
   uint16_t* x;      // [Tp, Dx] their states, zeros behind the last and past D
-  uint16_t* xr;     // [Tp, Dx] the same times dloss / g
-  float* lse;       // [Tp]
+  uint16_t* xr;     // [Tp, Dx] the same times 2^e and the sign
+  float* m;         // [Tp]
+  float* l2;        // [Tp] lse in bits, less log2 m
   int32_t* y;       // [Tp]
-  float* r;         // [T] dloss / g
-  float* cy;        // [T] c of the target
-  int32_t* uneven;  // [1] whether any r is no power of two
+  float* cy;        // [T] m c of the target
+  int32_t* uneven;  // [1] whether any m may differ from 1
 };
 
 struct CeParams {
@@ -456,17 +456,21 @@ __global__ __launch_bounds__(256) void k_ce_gather(CeParams p) {
   const uint4* const from = reinterpret_cast<const uint4*>(p.x + t * p.x_ld);
   uint4* const tor = reinterpret_cast<uint4*>(p.live.xr + i * p.Dx);
   const float r = live ? (p.dloss ? p.dloss[t] : 1.0f) / *p.live.g : 0.0f;
+  // a weight that is no number, or vanishes beside g, stands for itself
+  const bool split = __builtin_isfinite(r) && r != 0.0f;
+  const float m = split ? 2.0f * __builtin_amdgcn_frexp_mantf(fabsf(r)) : 1.0f;
+  const float e = split ? copysignf(ldexpf(1.0f, __builtin_amdgcn_frexp_expf(r) - 1), r) : r;
   for (int k = threadIdx.x; k < (int)(p.Dx / 8); k += 256) {
     uint4 q = make_uint4(0, 0, 0, 0);
     if (live && 8 * k < p.D) q = from[k];
     to[k] = q;
-    auto times = [&](uint32_t w) { return pack_bf16(bf16_lo(w) * r, bf16_hi(w) * r); };
+    auto times = [&](uint32_t w) { return pack_bf16(bf16_lo(w) * e, bf16_hi(w) * e); };
     tor[k] = make_uint4(times(q.x), times(q.y), times(q.z), times(q.w));
   }
   if (threadIdx.x == 0) {
-    p.live.lse[i] = live ? p.lse[t] : 0.0f;
+    p.live.m[i] = m;
+    p.live.l2[i] = (live ? p.lse[t] : 0.0f) * kLog2e - (m == 1.0f ? 0.0f : log2f(m));
     p.live.y[i] = live ? p.targets[t] : -1;
-    if (live) p.live.r[i] = r;
   }
 }
 
@@ -507,7 +511,7 @@ __device__ __forceinline__ void store_block(char* region, f32x16 (&acc)[kF][kF],
   }
 }
 
-// c of the piece, tile by tile: [live rows, Vp] bf16, zeros past V (rows behind
+// m c of the piece, tile by tile: [live rows, Vp] bf16, zeros past V (rows behind
 // the last hold anything).  8192 x 32768 out of 4096: 1.77 ms, 1.24 PFLOP/s.
 template <int kF, bool kTurn>
 __global__ __launch_bounds__(gemm::kThreads, kF == 4 ? 1 : 2) void k_ce_coef(CeParams p) {
@@ -534,19 +538,20 @@ __global__ __launch_bounds__(gemm::kThreads, kF == 4 ? 1 : 2) void k_ce_coef(CeP
         store_block<kF>(
             lds + 2048 * kF * wave, acc,
             [&](int j, float (&z)[kF][16]) {
-              const float l2 = p.live.lse[tw + 32 * j + l32] * kLog2e;
+              const float l2 = p.live.l2[tw + 32 * j + l32];
               const int y = (int)min<int64_t>((int64_t)p.live.y[tw + 32 * j + l32] - vw, kWave);
 #pragma unroll
               for (int i = 0; i < kF; ++i)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) z[i][v] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i][v], k2, -l2));
               if (__any(y >= 0 && y < kWave)) {
+                const float m = p.live.m[tw + 32 * j + l32];
                 float hit = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kF; ++i)
 #pragma unroll
                   for (int v = 0; v < 16; ++v)
-                    if (row_of(i, v) == y - 4 * h) hit = z[i][v] -= 1.0f;
+                    if (row_of(i, v) == y - 4 * h) hit = z[i][v] -= m;
                 if (y >= 0 && y < kWave && ((y >> 2) & 1) == h) p.live.cy[tw + 32 * j + l32] = hit;
               }
               if (have < kWave) {
@@ -603,6 +608,9 @@ __global__ __launch_bounds__(gemm::kThreads, 1) void k_ce_dx(CeParams p) {
       p.slices, &slice);
 }
 
+// What rounding to bf16 takes from a value (exactly).
+__device__ __forceinline__ float lost_of(float f) { return f - bf16_lo(pack_bf16(f, 0.0f)); }
+
 // dx of every token: its slices in order, zero for a token that does not count.
 // kSplit: a token's 256 columns take four waves, each a quarter of the slices
 // (many slices stand for few tokens; gradient of 20 tokens, 100000 words of 64:
@@ -636,31 +644,39 @@ __global__ __launch_bounds__(256) void k_ce_dx_join(CeParams p) {
     }
   }
   if (d >= p.D) return;
-  const float s = p.scale * (p.dloss ? p.dloss[t] : 1.0f);
+  if (i >= 0 && *p.live.uneven) {  // what the target's own m c lost, as add_targets() gives it to dw
+    const float lost = lost_of(p.live.cy[i]);
+    const uint2 w = *reinterpret_cast<const uint2*>(p.w + (int64_t)p.live.y[i] * p.w_ld + d);
+    o = make_float4(__builtin_fmaf(lost, bf16_lo(w.x), o.x), __builtin_fmaf(lost, bf16_hi(w.x), o.y),
+                    __builtin_fmaf(lost, bf16_lo(w.y), o.z), __builtin_fmaf(lost, bf16_hi(w.y), o.w));
+  }
+  const float s = i < 0 ? 0.0f : p.scale * ((p.dloss ? p.dloss[t] : 1.0f) / p.live.m[i]);
   *reinterpret_cast<uint2*>(p.dx + t * p.dx_ld + d) =
       i < 0 ? make_uint2(0, 0) : make_uint2(pack_bf16(o.x * s, o.y * s), pack_bf16(o.z * s, o.w * s));
 }
 
-// What the roundings of c and of the weighted x took from a target's own term of
-// dw, added to a tile's sums: cy r x - bf16(cy) bf16(r x), as three products of
-// bf16 values (cy r in two pieces, 2^-17), each in a slot of the contraction of
-// its own that only the target's word has a factor for.  That term is most of a
-// word's gradient, and where weights differ, x rounded once more would cost as
-// much as dw's own rounding does (1023 tokens, 50001 words of 1000: relative
-// error 2.5e-3 without this, 1.8e-3 with it, 1.7e-3 of the rounding alone; loss
-// and gradient 469 us without, 486 with).  Equal weights skip it.
+// What the rounding of m c took from a target's own term of dw, added to a tile's
+// sums: (m cy - bf16(m cy)) 2^e x as products of bf16 values (what the rounding of
+// the first factor takes is 2^-17 of the term), each in a slot of the contraction
+// of its own that only the target's word has a factor for.  That term is most of a
+// word's gradient, and dx gets back its own in k_ce_dx_join; equal weights skip
+// both.  1023 tokens, 50001 words of 1000, weighted: relative error of dw 2.37e-3
+// without this, 1.65e-3 with it, all of it dw's own rounding; of dx 2.37e-3 and
+// 1.66e-3; loss and gradient 496 and 502 us.  (A weight rounded into the rows of x
+// instead left words without a target at 2.30e-3 in fp32; as it is 1.63e-3, one
+// rounding of m c.)
 // The tokens of a tile's words are searched for each tile: n / 256 loads a
 // thread, where the products of n tokens took n / 64 stages of 2048 cycles.  Many
-// tokens of few words take several turns; tokens are added in their order.  Four
+// tokens of few words take several turns; tokens are added in their order.  16
 // tokens are one product of the contraction's smallest length, so few words cost
-// most (gradient of 8192 tokens, 5000 words of 1024: 317 us with equal weights, 348
-// with others; 1000 words: 179 and 276).
+// most (loss and gradient of 8192 tokens, 5000 words of 1024: 424 us with equal
+// weights, 449 with others; 1000 words: 210 and 271).
 template <int kF>
 __device__ __forceinline__ void add_targets(const CeParams& p, char* lds, int n, int64_t v0, int64_t d0, f32x16 (&acc)[kF][kF]) {
   constexpr int kWave = 32 * kF, kU = 2 * kF, kCap = 256 * kF;  // kCap: tokens of a wave's words that one wave finds in a turn
   struct Found {
     uint32_t key;  // token and word
-    float r, cy;
+    float lost;
   };
   const int lane = lane_here(), l32 = lane & 31, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int* const count = reinterpret_cast<int*>(lds);         // [2][4]
@@ -685,7 +701,7 @@ __device__ __forceinline__ void add_targets(const CeParams& p, char* lds, int n,
           const uint64_t mask = __ballot(in);
           if (in)
             list[(4 * s + wave) * kCap + have[s] + __popcll(mask & ((1ull << lane) - 1ull))] = {
-                (uint32_t)t << 7 | (uint32_t)(v - s * kWave), p.live.r[t], p.live.cy[t]};
+                (uint32_t)t << 7 | (uint32_t)(v - s * kWave), lost_of(p.live.cy[t])};
           have[s] += __popcll(mask);
         }
       }
@@ -698,54 +714,38 @@ __device__ __forceinline__ void add_targets(const CeParams& p, char* lds, int n,
     __syncthreads();
     const int* const mine = count + 4 * half;
     const int c1 = mine[0], c2 = c1 + mine[1], c3 = c2 + mine[2], all = __builtin_amdgcn_readfirstlane(c3 + mine[3]);
-    constexpr int kAhead = 4;  // products of four tokens each whose states are on their way together
-    for (int k0 = 0; k0 < all; k0 += 4 * kAhead) {
-      Found f[kAhead][2];  // this lane's half of a product's 16 slots: two tokens of four
-      uint32_t x[kAhead][2][kF];
+    for (int k0 = 0; k0 < all; k0 += 16) {
+      Found f[8];  // this lane's half of a product's slots
+      uint32_t x[8][kF];
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a)
+      for (int u = 0; u < 8; ++u) {
+        const int i = min(k0 + 8 * h + u, all - 1);
+        const int w = (i >= c1) + (i >= c2) + (i >= c3), first = w == 0 ? 0 : w == 1 ? c1 : w == 2 ? c2 : c3;
+        f[u] = list[(4 * half + w) * kCap + i - first];
+      }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int i = min(k0 + 4 * a + 2 * h + u, all - 1);
-          const int w = (i >= c1) + (i >= c2) + (i >= c3), first = w == 0 ? 0 : w == 1 ? c1 : w == 2 ? c2 : c3;
-          f[a][u] = list[(4 * half + w) * kCap + i - first];
-        }
+      for (int u = 0; u < 8; ++u)
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a)
+        for (int g = 0; g < kF; ++g)  // columns past D are not stored
+          x[u][g] = p.live.xr[(int64_t)(f[u].key >> 7) * p.Dx + min<int64_t>(d + 32 * g, p.D - 1)];
+      uint32_t wb[kF][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t both = pack_bf16(f[2 * q].lost, f[2 * q + 1].lost);
+        const int at0 = k0 + 8 * h + 2 * q;
+        const int word0 = at0 < all ? (int)(f[2 * q].key & 127u) : -1, word1 = at0 + 1 < all ? (int)(f[2 * q + 1].key & 127u) : -1;
 #pragma unroll
-          for (int g = 0; g < kF; ++g)  // columns past D are not stored
-            x[a][u][g] = p.live.x[(int64_t)(f[a][u].key >> 7) * p.Dx + min<int64_t>(d + 32 * g, p.D - 1)];
+        for (int j = 0; j < kF; ++j)
+          wb[j][q] = (word0 == 32 * j + l32 ? both & 0xFFFFu : 0u) | (word1 == 32 * j + l32 ? both & 0xFFFF0000u : 0u);
+      }
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        if (k0 + 4 * a >= all) break;
-        uint32_t wa[kF][4], wb[kF][4];
+      for (int g = 0; g < kF; ++g) {
+        const uint4 wa = make_uint4(x[0][g] | x[1][g] << 16, x[2][g] | x[3][g] << 16, x[4][g] | x[5][g] << 16, x[6][g] | x[7][g] << 16);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float r = f[a][u].r, cy = f[a][u].cy, cr = cy * r;
-          const uint32_t hi = pack_bf16(cr, cy), lo = pack_bf16(cr - bf16_lo(hi), 0.0f);
-          const int word = k0 + 4 * a + 2 * h + u < all ? (int)(f[a][u].key & 127u) : -1;
-#pragma unroll
-          for (int j = 0; j < kF; ++j) {
-            const bool hit = word == 32 * j + l32;
-            wb[j][2 * u] = hit ? (hi & 0xFFFFu) | lo << 16 : 0u;
-            wb[j][2 * u + 1] = hit ? (hi >> 16) ^ 0x8000u : 0u;
-          }
-#pragma unroll
-          for (int g = 0; g < kF; ++g) {
-            const uint32_t q = x[a][u][g];
-            wa[g][2 * u] = q | q << 16;
-            wa[g][2 * u + 1] = pack_bf16(bf16_lo(q) * r, 0.0f) & 0xFFFFu;
-          }
-        }
-#pragma unroll
-        for (int g = 0; g < kF; ++g)
-#pragma unroll
-          for (int j = 0; j < kF; ++j)
-            acc[g][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                __builtin_bit_cast(gemm::bf16x8, make_uint4(wa[g][0], wa[g][1], wa[g][2], wa[g][3])),
-                __builtin_bit_cast(gemm::bf16x8, make_uint4(wb[j][0], wb[j][1], wb[j][2], wb[j][3])), acc[g][j], 0, 0, 0);
+        for (int j = 0; j < kF; ++j)
+          acc[g][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              __builtin_bit_cast(gemm::bf16x8, wa),
+              __builtin_bit_cast(gemm::bf16x8, make_uint4(wb[j][0], wb[j][1], wb[j][2], wb[j][3])), acc[g][j], 0, 0, 0);
       }
     }
     const bool again = (more[0] | more[1] | more[2] | more[3]) != 0;
@@ -893,9 +893,9 @@ void backward_layout(void* ws, CeLayout& L) {
   p.live.pos = c.take<int32_t>((size_t)p.T);
   p.live.x = c.take<uint16_t>((size_t)(p.Tp * p.Dx));
   p.live.xr = c.take<uint16_t>((size_t)(p.Tp * p.Dx));
-  p.live.lse = c.take<float>((size_t)p.Tp);
+  p.live.m = c.take<float>((size_t)p.Tp);
+  p.live.l2 = c.take<float>((size_t)p.Tp);
   p.live.y = c.take<int32_t>((size_t)p.Tp);
-  p.live.r = c.take<float>((size_t)p.T);
   p.live.cy = c.take<float>((size_t)p.T);
   p.live.uneven = c.take<int32_t>(1);
   p.c = c.take<uint16_t>((size_t)(p.Tp * p.Vp));

@@ -366,3 +366,74 @@ def test_graphs_streams_and_a_shared_workspace():
                 assert torch.equal(a, b), rep
         step(sets[rep % 2], ws)  # eager work over the same workspace between the replays
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T,V", [(40, 500), (300, 700), (300, 30000), (48, 70000)])
+@pytest.mark.parametrize("weights", ["equal", "powers of two", "any"])
+def test_each_product_of_dw_is_rounded_once(T, V, weights):
+    """Every token has columns of its own, so an element of dw is one product c
+    dloss x: off by one rounding to bf16, of c and the weight together, whatever
+    the weights are (a second one, of the weighted state, would make it up to
+    2^-7), and by c's own error.  A target's own is good to 2^-15."""
+    import torch
+
+    nvq = _nvq()
+    log(f"[ce once] T={T} V={V} {weights}")
+    D = 8 * T
+    x, w, y, _ = _inputs(T, D, V, seed=6)
+    own = torch.arange(D, device="cuda") // 8 == torch.arange(T, device="cuda")[:, None]
+    x = torch.where(own, x, 0.0)
+    g = torch.Generator().manual_seed(T)
+    d = {"equal": torch.full((T,), 0.3), "any": torch.rand(T, generator=g) * 0.9 + 0.1,
+         "powers of two": 0.3 * 2.0 ** torch.randint(-9, 1, (T,), generator=g)}[weights]
+    d = (d * (torch.randint(0, 2, (T,), generator=g) * 2 - 1)).cuda()
+    _, lse = nvq.nvq_linear_cross_entropy(x, w, y)
+    _, got = nvq.nvq_linear_cross_entropy_backward(x, w, y, lse, d, want_dx=False, dw=torch.empty(V, D, device="cuda"))
+    part = w.reshape(V, T, 8)  # [word, token, its columns]
+    xs = x.reshape(T, T, 8).diagonal(dim1=0, dim2=1).T  # [token, its columns]
+    off, worst = 0.0, 0.0
+    for v0 in range(0, V, 10000):
+        words = torch.arange(v0, min(v0 + 10000, V), device="cuda")
+        p = part[words].double()
+        z = (p * xs.double()).sum(-1)  # [word, token]
+        dz = 9 * ref.ADD * (p * xs.double()).abs().sum(-1)
+        prob = torch.exp(z - lse.double())
+        hit = words[:, None] == y
+        c = prob - hit.double()
+        rel = dz + 8 * ref.U32 * (z.abs() + lse.double().abs()) + 4 * ref.U32  # of the given lse
+        want = (c * d.double())[:, :, None] * xs.double()
+        e_c = prob * rel + 4 * ref.U32 * c.abs()
+        e_c = e_c + (c.abs() + e_c) * torch.where(hit & (weights == "any"), 2.0 ** -15, ref.BF16)
+        room = (e_c * d.double().abs())[:, :, None] * xs.double().abs()
+        room = (room + 12 * ref.U32 * want.abs()).reshape(len(words), D)
+        ref.within(got[words], want.reshape(len(words), D), room, "dw")
+
+
+def test_weighted_dx_keeps_its_targets_term():
+    """w has one element in each target's row and none elsewhere: an element of
+    dx is one product c dloss w.  The target's own is as good as dx's rounding
+    lets it be, the others' are off by one more of c and the weight."""
+    import torch
+
+    nvq = _nvq()
+    T, V = 96, 3000
+    D = T
+    x, w, y, _ = _inputs(T, D, V, seed=8, weighted=True)
+    g = torch.Generator().manual_seed(5)
+    y = torch.randperm(V, generator=g)[:T].to(torch.int32).cuda()
+    w = torch.zeros_like(w)
+    w[y.long(), torch.arange(T, device="cuda")] = (torch.rand(T, generator=g) + 0.5).to(torch.bfloat16).cuda()
+    d = (torch.rand(T, generator=g) + 0.01).cuda()
+    _, lse = nvq.nvq_linear_cross_entropy(x, w, y)
+    dx, _ = nvq.nvq_linear_cross_entropy_backward(x, w, y, lse, d, want_dw=False)
+    wd = w[y.long(), torch.arange(T, device="cuda")].double()
+    z = x.double() * wd  # [token, target of column]
+    hit = torch.eye(T, dtype=torch.bool, device="cuda")
+    prob = torch.exp(z - lse.double()[:, None])
+    c = prob - hit.double()
+    rel = 4 * ref.ADD * z.abs() + 8 * ref.U32 * (z.abs() + lse.double()[:, None].abs()) + 4 * ref.U32
+    want = c * d.double()[:, None] * wd
+    e_c = prob * rel + 4 * ref.U32 * c.abs()
+    e_c = e_c + (c.abs() + e_c) * torch.where(hit, 2.0 ** -15, ref.BF16)
+    room = e_c * d.double()[:, None] * wd + 12 * ref.U32 * want.abs()
+    ref.within(dx, want, room + ref.BF16 * (want.abs() + room), "dx")
