@@ -671,6 +671,8 @@ int nvq_rms_norm_backward(const nvq_rms_norm_grad_args* args, void* stream);
  * x [T, D] and w [V, D] bf16, row strides in elements (0: D), rows 16-byte
  * aligned; targets [T] int32.  A negative target (padding) has loss 0; one >= V
  * too, and sets NVQ_STATUS_BAD_TARGET.  lse is written for every token.
+ * loss is the target's distance from the largest logit and what the others add
+ * to it, not the difference of two large numbers: it is never negative.
  * Products are summed in fp32, exponentials and sums are fp32.  A token with a
  * NaN or +inf logit has NaN results; logits of -inf weigh nothing.
  * loss and lse [T] fp32, each nullable (not both).

@@ -77,7 +77,7 @@ struct CeParams {
   uint32_t* status;
   // forward
   float2* part;     // [vocabulary tiles, T] (maximum in bits, sum)
-  float* at;        // [T] the target's logit
+  float* at;        // [T] the target's logit in bits
   // gradient
   Live live;
   int64_t Dx;       // row length of live.x
@@ -188,8 +188,8 @@ __global__ __launch_bounds__(gemm::kThreads, kF == 4 ? 1 : 2) void k_ce_forward(
 #pragma unroll
             for (int i = 0; i < kF; ++i)
 #pragma unroll
-              for (int v = 0; v < 16; ++v) hit = row_of(i, v) == y - 4 * h ? acc[i][j][v] : hit;
-            if (y >= 0 && y < have && ((y >> 2) & 1) == h) p.at[t] = hit * p.scale;
+              for (int v = 0; v < 16; ++v) hit = row_of(i, v) == y - 4 * h ? z[i][v] : hit;
+            if (y >= 0 && y < have && ((y >> 2) & 1) == h) p.at[t] = hit;
           }
           if (have < kWave) {
 #pragma unroll
@@ -328,8 +328,8 @@ __global__ __launch_bounds__(256, 2) void k_ce_few(CeParams p) {
       const int v = part + i * kPer;
       const float* const q = red + v * kPitch + tok;
       const float d = (q[0] + q[64 * kPitch]) + (q[128 * kPitch] + q[192 * kPitch]);
-      if (v0 + v == y && y < p.V) p.at[t0 + tok] = d * p.scale;
       z[i] = v0 + v < p.V ? d * k2 : -INFINITY;
+      if (v0 + v == y && y < p.V) p.at[t0 + tok] = z[i];
       top = __builtin_fmaxf(top, z[i]);
     }
     const float ref = top == -INFINITY ? 0.0f : top;
@@ -376,11 +376,15 @@ __global__ __launch_bounds__(1024) void k_ce_join(CeParams p, int parts) {
   if (part != 0 || t >= p.T) return;
 #pragma unroll
   for (int i = 1; i < 8; ++i) join(m, sum, s[i][l]);
-  const float lse = m * kLn2 + logf(sum);
-  if (p.lse) p.lse[t] = lse;
+  // The loss is the target's distance from the maximum, in bits, and what the sum
+  // adds to it, never the difference of two large numbers: a token whose target
+  // leads has the loss that the others leave it, and none is negative (tokens with
+  // logits of 2000 were off by 1.2e-4 as lse - logit).
+  const float rest = logf(sum);
+  if (p.lse) p.lse[t] = m * kLn2 + rest;
   const int64_t y = p.targets[t];
   if (y >= p.V) atomicOr(p.status, (uint32_t)NVQ_STATUS_BAD_TARGET);
-  if (p.loss) p.loss[t] = y >= 0 && y < p.V ? lse - p.at[t] : 0.0f;
+  if (p.loss) p.loss[t] = y >= 0 && y < p.V ? (m - p.at[t]) * kLn2 + rest : 0.0f;
 }
 
 // --------------------------------------------------------------- gradient --

@@ -437,3 +437,41 @@ def test_weighted_dx_keeps_its_targets_term():
     e_c = e_c + (c.abs() + e_c) * torch.where(hit, 2.0 ** -15, ref.BF16)
     room = e_c * d.double()[:, None] * wd + 12 * ref.U32 * want.abs()
     ref.within(dx, want, room + ref.BF16 * (want.abs() + room), "dx")
+
+
+@pytest.mark.parametrize("T,V", [(20, 300), (300, 5000)])
+def test_losses_of_sure_tokens(T, V):
+    """Logits of thousands whose target leads by up to forty: the loss is the
+    others' share, not the difference of two large numbers.  It is never
+    negative, and off by the sums of exponentials' roundings (130, as the bound
+    of the log-sum-exp counts them), three of its own, and the logits' own error
+    times that share."""
+    import torch
+
+    nvq = _nvq()
+    log(f"[ce sure] T={T} V={V}")
+    D = 8 + -(-T // 8) * 8
+    g = torch.Generator().manual_seed(9)
+    t = torch.arange(T)
+    w = torch.randint(-2, 3, (V, D), generator=g).to(torch.bfloat16)
+    y = torch.randperm(V, generator=g)[:T].to(torch.int32)
+    x = torch.zeros(T, D)
+    x[:, 0] = 32.0 + t % 4          # times 64: what all logits of half the vocabulary have in common
+    x[t, 8 + t] = (t % 11) / 32.0   # times 120: the target's lead
+    x = x.to(torch.bfloat16)
+    w[:V // 2, 0] = 64.0
+    w[y.long(), 0] = 64.0
+    w[y.long(), 8 + t] = 120.0
+    x, w, y = x.cuda(), w.cuda(), y.cuda()
+    loss, lse = nvq.nvq_linear_cross_entropy(x, w, y)
+    # every logit is exact in fp32: two products of few bits
+    z = x.double() @ w.double().T
+    assert torch.equal(z, z.float().double()) and float(z.max()) > 2000
+    at = z.gather(1, y.long()[:, None])
+    want = torch.log1p(torch.exp(z - at).sum(-1) - 1.0)
+    share = 1 - torch.exp(-want.clamp(min=0))
+    # of a logit: its product with log2(e), and the subtraction
+    arg = 4 * ref.U32 * z.abs().amax(-1)
+    room = 130 * ref.U32 + 4 * ref.U32 * want.abs() + share * arg
+    assert bool((loss >= 0).all())
+    ref.within(loss, want, room, "loss")
