@@ -475,3 +475,175 @@ def test_losses_of_sure_tokens(T, V):
     room = 130 * ref.U32 + 4 * ref.U32 * want.abs() + share * arg
     assert bool((loss >= 0).all())
     ref.within(loss, want, room, "loss")
+
+
+# what the kernel for few tokens does not take: as quarters of tiles, as whole
+# ones, as whole ones in one column
+TILED = [(300, 5000), (520, 15001), (250, 40001)]
+TILED_SIZES = [(255, 64, 16385), (257, 72, 5120), (256, 128, 25599), (513, 64, 11009), (130, 2056, 8193), (600, 1000, 8000),
+               (64, 264, 41000), (65, 64, 33000)]
+
+
+@pytest.mark.parametrize("T,D,V", TILED_SIZES)
+@pytest.mark.parametrize("scale,ignore,weighted", [(1.0, 0, False), (0.7, 3, True)])
+def test_tiled_loss_and_gradient_match_64_bits(T, D, V, scale, ignore, weighted):
+    test_loss_and_gradient_match_64_bits(T, D, V, scale, ignore, weighted)
+
+
+@pytest.mark.parametrize("T,V", TILED)
+def test_tiled_strided_rows(T, V):
+    import torch
+
+    nvq = _nvq()
+    log(f"[ce tiled strided] T={T} V={V}")
+    D = 72
+    x, w, y, d = _inputs(T, D, V, ignore=7, weighted=True)
+    loss, lse = nvq.nvq_linear_cross_entropy(x, w, y)
+    dx, dw = nvq.nvq_linear_cross_entropy_backward(x, w, y, lse, d)
+
+    def wide(t, pad):
+        b = torch.full((t.shape[0], t.shape[1] + 2 * pad), float("nan"), dtype=t.dtype, device="cuda")
+        b[:, pad:-pad] = t
+        return b, b[:, pad:-pad]
+
+    (_, xs), (_, wsd) = wide(x, 8), wide(w, 24)
+    loss2, lse2 = nvq.nvq_linear_cross_entropy(xs, wsd, y)
+    assert torch.equal(loss, loss2) and torch.equal(lse, lse2)
+    for dtype in (torch.bfloat16, torch.float32):
+        (bx, dxs), (bw, dws) = wide(dx, 16), wide(dw.to(dtype), 8)
+        for accumulate in (False, True):
+            dws[:] = 0.0 if accumulate else 7.0
+            nvq.nvq_linear_cross_entropy_backward(xs, wsd, y, lse, d, dx=dxs, dw=dws, accumulate=accumulate)
+            assert torch.equal(dxs, dx) and torch.equal(dws.to(torch.bfloat16), dw)
+            for b, pad in ((bx, 16), (bw, 8)):
+                assert bool(b[:, :pad].isnan().all()) and bool(b[:, -pad:].isnan().all())
+
+
+@pytest.mark.parametrize("T,V", TILED)
+def test_tiled_padded_tokens_and_bad_targets(T, V):
+    import torch
+
+    nvq = _nvq()
+    L = nvq.load()
+    log(f"[ce tiled padded] T={T} V={V}")
+    D = 96
+    x, w, y, d = _inputs(T, D, V, weighted=True)
+    y[5:40] = -1
+    y[T - 1] = -100
+    loss, lse = nvq.nvq_linear_cross_entropy(x, w, y)
+    dx, dw = nvq.nvq_linear_cross_entropy_backward(x, w, y, lse, d)
+    assert bool((loss[y < 0] == 0).all()) and bool((dx[y < 0] == 0).all())
+    bad = y.clone()
+    bad[7], bad[T - 1], bad[39] = V, 2 ** 31 - 1, V + 255
+    x2, lse2 = x.clone(), lse.clone()
+    x2[y < 0] = float("nan")
+    lse2[y < 0] = float("nan")
+    ws = nvq.workspace(max(L.nvq_linear_cross_entropy_workspace_bytes(T, D, V),
+                           L.nvq_linear_cross_entropy_backward_workspace_bytes(T, D, V)), x.device)
+    live = y >= 0
+    for targets, status in ((bad, nvq.NVQ_STATUS_BAD_TARGET), (y, 0)):
+        ws.fill_(255)
+        loss2, lse3 = nvq.nvq_linear_cross_entropy(x2, w, targets, ws=ws)
+        assert nvq.device_status(ws) == status
+        assert torch.equal(loss2, loss) and torch.equal(lse3[live], lse[live]) and bool(lse3[~live].isnan().all())
+        ws.fill_(255)
+        dx2, dw2 = nvq.nvq_linear_cross_entropy_backward(x2, w, targets, lse2, d, ws=ws)
+        assert nvq.device_status(ws) == status
+        assert torch.equal(dx2, dx) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("T,V", TILED)
+def test_tiled_extreme_logits(T, V):
+    import torch
+
+    nvq = _nvq()
+    log(f"[ce tiled extreme] T={T} V={V}")
+    D = 64
+    x, w, y, d = _inputs(T, D, V)
+    for scale in (300.0, -0.5, 0.0):
+        (loss, lse, dx, dw), (e_loss, e_lse, e_dx, e_dw) = ref.cross_entropy(x, w, y, scale, d)
+        got, got_lse = nvq.nvq_linear_cross_entropy(x, w, y, scale=scale)
+        ref.within(got, loss, e_loss, "loss")
+        ref.within(got_lse, lse, e_lse, "lse")
+        if scale != 300.0:
+            got_dx, got_dw = nvq.nvq_linear_cross_entropy_backward(x, w, y, got_lse, d, scale=scale)
+            ref.within(got_dx, dx, e_dx, "dx")
+            ref.within(got_dw, dw, e_dw + ref.BF16 * (dw.abs() + e_dw), "dw")
+    # words of logit -inf weigh nothing: some, a whole block of 128 words, the last ones
+    keep = torch.ones(V, dtype=torch.bool, device="cuda")
+    keep[100:120] = False
+    keep[256:512] = False
+    keep[V - 3:] = False
+    w2, x2 = w.clone(), x.clone()
+    w2[~keep, 5] = float("-inf")
+    x2[:, 5] = 1.0
+    y2 = torch.where(keep[y.long()], y, 7).to(torch.int32)
+    moved = (torch.cumsum(keep, 0) - 1)[y2.long()].to(torch.int32)
+    (loss, lse, _, _), (e_loss, e_lse, _, _) = ref.cross_entropy(x2, w2[keep], moved, 1.0)
+    got, got_lse = nvq.nvq_linear_cross_entropy(x2, w2, y2)
+    ref.within(got, loss, e_loss, "loss beside -inf")
+    ref.within(got_lse, lse, e_lse, "lse beside -inf")
+    # nothing but -inf: the log-sum-exp of an empty sum, and no loss
+    x3 = x.clone()
+    x3[0], x3[T - 1] = 0.0, 0.0
+    x3[0, 0], x3[T - 1, 0] = float("-inf"), float("-inf")
+    w3 = w.clone()
+    w3[:, 0] = w3[:, 0].abs() + 0.5
+    base, base_lse = nvq.nvq_linear_cross_entropy(x, w3, y)
+    got, got_lse = nvq.nvq_linear_cross_entropy(x3, w3, y)
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    rest[0] = rest[T - 1] = False
+    assert bool((got_lse[~rest] == float("-inf")).all()) and bool(got[~rest].isnan().all())
+    assert torch.equal(got[rest], base[rest]) and torch.equal(got_lse[rest], base_lse[rest])
+    # NaN and +inf stay with their tokens
+    x4 = x.clone()
+    x4[11, 0] = float("nan")
+    x4[T - 2] = 0.0
+    x4[T - 2, 0] = float("inf")
+    got, got_lse = nvq.nvq_linear_cross_entropy(x4, w3, y)
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    rest[11] = rest[T - 2] = False
+    assert bool(got[~rest].isnan().all()) and bool(got_lse[~rest].isnan().all())
+    assert torch.equal(got[rest], base[rest]) and torch.equal(got_lse[rest], base_lse[rest])
+
+
+def test_tiled_graphs_streams_and_a_shared_workspace():
+    import torch
+
+    nvq = _nvq()
+    L = nvq.load()
+    D = 128
+    sets = [_inputs(T, D, V, seed=k, weighted=k == 1, ignore=4 * (k % 2)) for k, (T, V) in enumerate(TILED)]
+    ws = nvq.workspace(max(max(L.nvq_linear_cross_entropy_workspace_bytes(T, D, V),
+                               L.nvq_linear_cross_entropy_backward_workspace_bytes(T, D, V)) for T, V in TILED), "cuda")
+
+    def step(s, ws):
+        x, w, y, d = s
+        loss, lse = nvq.nvq_linear_cross_entropy(x, w, y, ws=ws)
+        return loss, lse, *nvq.nvq_linear_cross_entropy_backward(x, w, y, lse, d, ws=ws)
+
+    eager = [[t.clone() for t in step(s, None)] for s in sets]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for s, e in zip(sets, eager):
+            for a, b in zip(step(s, ws), e):
+                assert torch.equal(a, b)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs = []
+    for s in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs = step(s, ws)
+        graphs.append((g, outs))
+    for rep in range(3):
+        for (g, outs), e in zip(graphs, eager):
+            for t in outs:
+                t.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(outs, e):
+                assert torch.equal(a, b), rep
+        step(sets[rep % 3], ws)  # eager work over the same workspace between the replays
+        torch.cuda.synchronize()

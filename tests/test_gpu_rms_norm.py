@@ -353,3 +353,23 @@ def test_eight_bit_nan_of_any_payload(group, dtype, bits):
     assert bool(codes.float().reshape(T, D // n, n)[:, hit].isnan().all()) and bool(scales[:, hit].isnan().all())
     assert torch.equal(c[:, ~hit], clean.view(torch.uint8).reshape(T, D // n, n)[:, ~hit])
     assert torch.equal(scales[:, ~hit], clean_scales[:, ~hit])
+
+
+@pytest.mark.parametrize("D,group", [(512, 128), (512, 32), (4096, 64), (1000, 0), (24, 0)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_both_outputs_of_one_call(D, group, dtype):
+    """y beside its codes, as the argument structure allows, with the norm's
+    maximum: the bits of two calls."""
+    import torch
+
+    nvq = _nvq()
+    T = 41
+    x, res, _, _, w = _inputs(T, D, dtype, "float32", seed=31)
+    amax, amax2 = torch.zeros(1, device="cuda"), torch.full((1,), 5.0, device="cuda")
+    y, h, r = nvq.nvq_rms_norm(x, w, residual=res, want_rstd=True, out_amax=amax)
+    codes, scales, _, _ = nvq.nvq_rms_norm_e4m3(x, w, residual=res, group=group)
+    y2, h2 = torch.zeros_like(y), torch.zeros_like(h)
+    codes2, scales2 = torch.zeros_like(codes), torch.zeros_like(scales)
+    _, _, r2 = nvq._norm(x, w, 1e-6, res, True, y2, h2, codes2, scales2, group, amax2)
+    for a, b in ((y, y2), (h, h2), (r, r2), (codes.view(torch.uint8), codes2.view(torch.uint8)), (scales, scales2), (amax, amax2)):
+        assert torch.equal(a, b)

@@ -239,3 +239,16 @@ sys.exit(0 if got == [-4, -4, -4, -1, -4, -4, -4, -1, -1, -1] else repr(got))
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", program], capture_output=True, text=True, cwd=root)
     assert r.returncode == 0, r.stderr[-500:]
+
+
+def test_the_tiled_sizes_go_to_tiles():
+    """The kernel for few tokens leaves a partial result (8 bytes a token) for each
+    64 words, up to 512, tiles one for each 128: the workspace tells which it is."""
+    from test_gpu_linear_ce import TILED, TILED_SIZES
+
+    L = _lib()
+    for T, D, V in [(T, 64, V) for T, V in TILED] + TILED_SIZES:
+        tiles, few = (V + 127) // 128, min((V + 63) // 64, 512)
+        assert 8 * T * tiles <= L.nvq_linear_cross_entropy_workspace_bytes(T, D, V) < 8 * T * few, (T, D, V)
+    for T, D, V in [(40, 64, 5000), (300, 64, 1000)]:
+        assert 8 * T * min((V + 63) // 64, 512) <= L.nvq_linear_cross_entropy_workspace_bytes(T, D, V)
