@@ -182,7 +182,7 @@ __global__ __launch_bounds__(gemm::kThreads, kF == 4 ? 1 : 2) void k_ce_forward(
           for (int i = 0; i < kF; ++i)
 #pragma unroll
             for (int v = 0; v < 16; ++v) z[i][v] = acc[i][j][v] * k2;
-          const int y = t < p.T ? (int)min<int64_t>(p.targets[t] - vw, kWave) : -1;
+          const int y = t < p.T ? (int)min<int64_t>(p.targets[t] - vw, (int64_t)kWave) : -1;
           if (__any(y >= 0 && y < have)) {
             float hit = 0.0f;
 #pragma unroll
@@ -543,7 +543,7 @@ __global__ __launch_bounds__(gemm::kThreads, kF == 4 ? 1 : 2) void k_ce_coef(CeP
             lds + 2048 * kF * wave, acc,
             [&](int j, float (&z)[kF][16]) {
               const float l2 = p.live.l2[tw + 32 * j + l32];
-              const int y = (int)min<int64_t>((int64_t)p.live.y[tw + 32 * j + l32] - vw, kWave);
+              const int y = (int)min<int64_t>(p.live.y[tw + 32 * j + l32] - vw, (int64_t)kWave);
 #pragma unroll
               for (int i = 0; i < kF; ++i)
 #pragma unroll
