@@ -21,7 +21,7 @@
 // products of m c with w and with 2^e x.  dx is summed in fp32 over the pieces.
 //
 // Bound by the matrix cores' power: 8192 tokens, 65536 words of 4096 (four
-// products of 4.4 TFLOP) take 3.3 + 10.5 ms, 1.27 PFLOP/s over all of it, the
+// products of 4.4 TFLOP) take 3.3 + 10.5 ms (3.4 + 10.9 on another card), 1.27 PFLOP/s, the
 // tiles of 256 alone 1.33 (forward), 1.23 (c), 1.31 (dx) and 1.29 (dw).  Few
 // tokens are bound by w's bytes: one token, 131072 words of 7168, 309 us (6.1 TB/s).
 
